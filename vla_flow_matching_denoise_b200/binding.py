@@ -26,14 +26,17 @@ FM_W_W8A8_E4M3 = 3
 STATUS = {0: "FM_OK", 1: "FM_ERR_INVALID_ARG", 2: "FM_ERR_NOT_READY", 3: "FM_ERR_OOM",
           4: "FM_ERR_CUDA", 5: "FM_ERR_TIMEOUT", 6: "FM_ERR_UNSUPPORTED"}
 
-# Every symbol include/fm_expert.h declares.
+# Every symbol include/fm_expert.h and include/fm_ops.h declare.
 EXPORTS = ("fm_expert_create", "fm_set_prefix", "fm_set_prefix_varlen", "fm_set_prefix_builder",
            "fm_build_prefix", "fm_get_prefix_kv", "fm_get_nvfp4_weights", "fm_quantize_act_e4m3", "fm_denoise", "fm_velocity", "fm_time_modulation",
            "fm_trace_bytes", "fm_trace_velocity", "fm_trace_batched_bytes", "fm_trace_batched",
            "fm_get_fp8_weights", "fm_sync", "fm_test_stall",
            "fm_get_geometry", "fm_profile_denoise", "fm_profile_phases", "fm_time_modulation_noalloc",
            "fm_expert_destroy", "fm_last_error", "fm_status_string",
-           "fm_abi_version")
+           "fm_abi_version",
+           # include/fm_ops.h
+           "fm_add_rmsnorm_e4m3", "fm_gated_e4m3", "fm_quantize_weight_e4m3_b128", "fm_gemm_e4m3_b128",
+           "fm_rope_axes", "fm_ops_sync")
 
 
 class FmConfig(ctypes.Structure):
@@ -108,11 +111,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fm_status_string.argtypes = [ip]
     lib.fm_status_string.restype = ctypes.c_char_p
     lib.fm_abi_version.restype = ip
+    ll, fl = ctypes.c_int64, ctypes.c_float
+    lib.fm_add_rmsnorm_e4m3.argtypes = [vp, ip, ll, vp, ip, ll, vp, fl, fl, ip, ip, vp, ll, vp, ll, vp, ll, vp]
+    lib.fm_gated_e4m3.argtypes = [vp, ip, ll, ip, ip, ip, vp, ll, vp, ll, vp]
+    lib.fm_quantize_weight_e4m3_b128.argtypes = [vp, ll, ip, ip, vp, ll, vp, ll, vp]
+    lib.fm_gemm_e4m3_b128.argtypes = [vp, ll, vp, ll, vp, ll, vp, ll, vp, ip, ip, ip, vp, ip, ll, vp]
+    lib.fm_rope_axes.argtypes = [vp, ip, ll, ip, ip, ip, ip, vp, ll, ip, vp, vp, ip, vp, ll, vp, ll, vp, ll, vp]
+    lib.fm_ops_sync.argtypes = [vp]
     for name in ("fm_expert_create", "fm_set_prefix", "fm_denoise", "fm_velocity",
                  "fm_time_modulation", "fm_trace_velocity", "fm_get_fp8_weights", "fm_sync",
                  "fm_test_stall", "fm_trace_batched", "fm_get_geometry", "fm_profile_denoise", "fm_profile_phases", "fm_time_modulation_noalloc",
                  "fm_set_prefix_varlen", "fm_set_prefix_builder", "fm_build_prefix", "fm_get_prefix_kv",
-                 "fm_get_nvfp4_weights", "fm_quantize_act_e4m3"):
+                 "fm_get_nvfp4_weights", "fm_quantize_act_e4m3", "fm_add_rmsnorm_e4m3", "fm_gated_e4m3",
+                 "fm_quantize_weight_e4m3_b128", "fm_gemm_e4m3_b128", "fm_rope_axes", "fm_ops_sync"):
         getattr(lib, name).restype = ip
     _lib = lib
     return lib

@@ -1,0 +1,632 @@
+// The E4M3 block-scaled operators of include/fm_ops.h that are bound by memory:
+// residual + RMS norm, the gated activation (both quantise their result),
+// the weight quantiser and the multi-axis RoPE.  The matrix product is in
+// fm_ops_gemm.cu.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdarg>
+#include <cstdint>
+#include <cstdio>
+
+#include "../../include/fm_ops.h"
+#include "fm_ops_check.h"
+#include "fm_ptx.cuh"
+
+namespace fm {
+namespace {
+
+// ----------------------------------------------------------------- 8 elements at a time
+template <typename T>
+struct Pack8;
+template <>
+struct Pack8<uint16_t> {   // bf16 bits
+  uint4 r;
+  __device__ __forceinline__ void load(const uint16_t* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Pack8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ float to_f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ float to_f(float f) { return f; }
+__device__ __forceinline__ void from_f(uint16_t* p, float v) {
+  const __nv_bfloat16 b = __float2bfloat16_rn(v);
+  *p = *reinterpret_cast<const uint16_t*>(&b);
+}
+__device__ __forceinline__ void from_f(float* p, float v) { *p = v; }
+
+// ----------------------------------------------------------------- group of 128 -> codes + scale
+// Half a warp holds one group of 128 values, 8 per lane (`live` false: none, the
+// group's ragged end).  a' = max(a, 2^-100) keeps 448 / a' finite, so tiny
+// groups give codes and not 0 x inf.
+constexpr float kTiny = 7.8886090522101181e-31f;   // 2^-100
+__device__ __forceinline__ void quantize_group(const float (&y)[8], bool live, int lane, uint8_t* code, float* scale) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(y[i]));
+#pragma unroll
+  for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  const float t = fmaxf(a, kTiny);
+  const float r = a > 0.f ? __fdiv_rn(448.0f, t) : 1.0f;
+  if (live) {
+    uint2 c;
+    c.x = f32x2_to_e4m3x2(__fmul_rn(y[0], r), __fmul_rn(y[1], r)) |
+          (f32x2_to_e4m3x2(__fmul_rn(y[2], r), __fmul_rn(y[3], r)) << 16);
+    c.y = f32x2_to_e4m3x2(__fmul_rn(y[4], r), __fmul_rn(y[5], r)) |
+          (f32x2_to_e4m3x2(__fmul_rn(y[6], r), __fmul_rn(y[7], r)) << 16);
+    *reinterpret_cast<uint2*>(code) = c;
+    if ((lane & 15) == 0) *scale = a > 0.f ? __fdiv_rn(t, 448.0f) : 1.0f;
+  }
+}
+
+// ----------------------------------------------------------------- residual + RMS norm
+// A row stays in the registers of its `wpr` warps between the sum of squares
+// and the codes: one pass over memory, 8 elements per lane and piece.
+struct NormParams {
+  const void* x;
+  const void* res;
+  const uint16_t* gain;
+  void* h;
+  uint8_t* codes;
+  float* scales;
+  int64_t ldx, ldr, ldh, ldc, lds;
+  float offset, eps;
+  int rows, d, wpr;
+};
+
+template <typename TX, typename TH, int NP>
+__global__ void norm_kernel(const NormParams p) {
+  __shared__ float part[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int slot = warp / p.wpr;                              // row of this block
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / (32 * p.wpr)) + slot;
+  const bool have = row < p.rows;
+  const int t = (warp - slot * p.wpr) * 32 + lane;            // thread of the row
+  const int pieces = p.d >> 3, step = p.wpr * 32;
+  const TX* x = static_cast<const TX*>(p.x) + row * p.ldx;
+  const TH* res = static_cast<const TH*>(p.res) + row * p.ldr;
+
+  float v[NP][8];
+  float sq = 0.f;
+  {
+    Pack8<TX> px[NP];
+    Pack8<TH> pr[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = t + i * step;
+      if (have && c < pieces) {
+        px[i].load(x + c * 8);
+        if (p.res != nullptr) pr[i].load(res + c * 8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = t + i * step;
+      if (have && c < pieces) {
+        px[i].get(v[i]);
+        if (p.res != nullptr) {
+          float r[8];
+          pr[i].get(r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] += r[e];
+        }
+        if (p.h != nullptr) store8(static_cast<TH*>(p.h) + row * p.ldh + c * 8, v[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sq = fmaf(v[i][e], v[i][e], sq);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+  if (p.wpr > 1) {
+    if (lane == 0) part[warp] = sq;
+    __syncthreads();
+    sq = 0.f;
+    for (int w = 0; w < p.wpr; ++w) sq += part[slot * p.wpr + w];
+  }
+  const float rstd = rsqrtf(sq / (float)p.d + p.eps);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int c = t + i * step;
+    if (i * step >= pieces) break;                            // the same for every lane
+    const bool live = have && c < pieces;
+    float g[8];
+    if (p.gain != nullptr && live) {
+      Pack8<uint16_t> pg;
+      pg.load(p.gain + c * 8);
+      pg.get(g);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = 1.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * rstd * (g[e] + p.offset);
+    quantize_group(v[i], live, lane, p.codes + row * p.ldc + c * 8, p.scales + row * p.lds + (c >> 4));
+  }
+}
+
+template <typename TX, typename TH>
+cudaError_t launch_norm(NormParams p, cudaStream_t st) {
+  // One piece of 8 per lane and row needs wpr = d / 256 warps; four pieces per
+  // lane quarter that.
+  const int pieces = p.d >> 3;
+  int np = pieces > 32 * 16 * 2 ? 4 : pieces > 32 * 16 ? 2 : 1;
+  if (p.rows > 512) np = 4;
+  p.wpr = (pieces + 32 * np - 1) / (32 * np);
+  const int rpb = p.wpr >= 8 ? 1 : 8 / p.wpr;
+  const unsigned grid = (unsigned)(((int64_t)p.rows + rpb - 1) / rpb);
+  const int threads = rpb * p.wpr * 32;
+  if (np == 1)
+    norm_kernel<TX, TH, 1><<<grid, threads, 0, st>>>(p);
+  else if (np == 2)
+    norm_kernel<TX, TH, 2><<<grid, threads, 0, st>>>(p);
+  else
+    norm_kernel<TX, TH, 4><<<grid, threads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+// ----------------------------------------------------------------- gated activation
+struct GatedParams {
+  const void* x;
+  uint8_t* codes;
+  float* scales;
+  int64_t ldx, ldc, lds;
+  int rows, f;
+  int row_pieces;          // pieces of 8 per row, rounded up to whole groups
+  int tiles;               // column tiles of blockDim.x pieces per row, or 0:
+  int rpb;                 //   so many whole rows per block
+};
+
+template <int ACT>
+__device__ __forceinline__ float gated(float g, float u) {
+  if (ACT == FM_ACT_SILU) return g / (1.0f + __expf(-g)) * u;
+  // 1 + tanh(z) = 2 / (1 + exp(-2 z)): no cancellation for negative z
+  const float z = 0.7978845608028654f * fmaf(0.044715f * g * g, g, g);
+  return g / (1.0f + __expf(-2.0f * z)) * u;
+}
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(256) gated_kernel(const GatedParams p) {
+  const int lane = threadIdx.x & 31;
+  int64_t row;
+  int c;
+  bool live = true;
+  if (p.tiles) {
+    row = blockIdx.x / (unsigned)p.tiles;
+    c = (blockIdx.x % (unsigned)p.tiles) * blockDim.x + threadIdx.x;
+  } else {
+    const int slot = threadIdx.x / p.row_pieces;     // the block's threads are rounded up to whole warps
+    live = slot < p.rpb;
+    row = (int64_t)blockIdx.x * p.rpb + slot;
+    c = threadIdx.x - slot * p.row_pieces;
+  }
+  live = live && row < p.rows && c * 8 < p.f;
+  float y[8];
+  if (live) {
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx + (int64_t)c * 8;
+    Pack8<T> a, b;
+    a.load(x);
+    if (ACT != FM_ACT_NONE) b.load(x + p.f);
+    a.get(y);
+    if (ACT != FM_ACT_NONE) {
+      float u[8];
+      b.get(u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = gated<ACT>(y[e], u[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = 0.f;
+  }
+  quantize_group(y, live, lane, p.codes + row * p.ldc + (int64_t)c * 8, p.scales + row * p.lds + (c >> 4));
+}
+
+template <typename T>
+cudaError_t launch_gated(GatedParams p, fm_act act, cudaStream_t st) {
+  p.row_pieces = ((p.f + 127) / 128) * 16;
+  int threads = 256;
+  int64_t grid;
+  if (p.row_pieces >= 256) {
+    p.tiles = (p.row_pieces + 255) / 256;
+    p.rpb = 0;
+    grid = (int64_t)p.rows * p.tiles;
+  } else {
+    p.tiles = 0;
+    p.rpb = 256 / p.row_pieces;
+    threads = (p.rpb * p.row_pieces + 31) & ~31;
+    grid = ((int64_t)p.rows + p.rpb - 1) / p.rpb;
+  }
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  if (act == FM_ACT_SILU)
+    gated_kernel<T, FM_ACT_SILU><<<(unsigned)grid, threads, 0, st>>>(p);
+  else if (act == FM_ACT_GELU_TANH)
+    gated_kernel<T, FM_ACT_GELU_TANH><<<(unsigned)grid, threads, 0, st>>>(p);
+  else
+    gated_kernel<T, FM_ACT_NONE><<<(unsigned)grid, threads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+// ----------------------------------------------------------------- weight quantiser
+// One block of threads per 128 x 128 block of the weight (a set-up call: two
+// reads of the block, the second from L1).
+__global__ void __launch_bounds__(256) quantize_weight_kernel(const uint16_t* __restrict__ w, int64_t ldw, int n, int k,
+                                                              uint8_t* __restrict__ codes, int64_t ldc,
+                                                              float* __restrict__ scales, int64_t lds) {
+  __shared__ float part[8];
+  const unsigned gk = (unsigned)((k + 127) / 128);
+  const int64_t n0 = (int64_t)(blockIdx.x / gk) * 128;
+  const int k0 = (int)(blockIdx.x % gk) * 128;
+  const int col = k0 + (threadIdx.x & 127);
+  const int r0 = threadIdx.x >> 7;
+  float a = 0.f;
+  if (col < k)
+    for (int r = r0; r < 128 && n0 + r < n; r += 2) a = fmaxf(a, fabsf(to_f(w[(n0 + r) * ldw + col])));
+  for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = fmaxf(a, part[i]);
+  const float s = a > 0.f ? __fdiv_rn(fmaxf(a, kTiny), 448.0f) : 1.0f;
+  if (threadIdx.x == 0) scales[(n0 / 128) * lds + blockIdx.x % gk] = s;
+  if (col < k)
+    for (int r = r0; r < 128 && n0 + r < n; r += 2)
+      codes[(n0 + r) * ldc + col] =
+          (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(to_f(w[(n0 + r) * ldw + col]), s), __NV_SATFINITE, __NV_E4M3);
+}
+
+// ----------------------------------------------------------------- multi-axis RoPE
+// The cosines and sines of a tile of rows are made once, in shared memory, for
+// all of its heads; the angle is reduced to a fraction of a turn in 64 bits
+// (positions x frequency passes 2^20 turns, where fp32 has no digits left).
+constexpr int kMaxPairs = 128;
+struct RopeParams {
+  const void* x;
+  const int32_t* pos;
+  void *q, *k, *v;
+  int64_t ldx, ldp, ldq, ldk, ldv;
+  int rows, nq, nkv, hd, n, tt;       // tt: rows per tile
+  double turn[kMaxPairs];             // frequency in turns per position
+  uint8_t axis[kMaxPairs];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
+  if constexpr (V == 8) {
+    Pack8<T> a;
+    a.load(p);
+    a.get(v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = to_f(p[i]);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
+  if constexpr (V == 8) {
+    store8(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) from_f(p + i, v[i]);
+  }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ float2 cs[];      // [tt][n]
+  __shared__ double turn[kMaxPairs];
+  __shared__ uint8_t axis[kMaxPairs];
+  const int tid = threadIdx.x, n = p.n;
+  for (int j = tid; j < n; j += blockDim.x) {
+    turn[j] = p.turn[j];
+    axis[j] = p.axis[j];
+  }
+  const int heads = p.nq + p.nkv;
+  const int rot = n / V, tail = (p.hd - 2 * n) / V, val = p.v != nullptr ? p.nkv * (p.hd / V) : 0;
+  const int u_rot = heads * rot, u_tail = heads * tail, units = u_rot + u_tail + val;
+  for (int64_t r0 = (int64_t)blockIdx.x * p.tt; r0 < p.rows; r0 += (int64_t)gridDim.x * p.tt) {
+    const int tt = (int)(p.rows - r0 < p.tt ? p.rows - r0 : p.tt);
+    __syncthreads();                  // the tables above; the previous tile's cs
+    for (int i = tid; i < tt * n; i += blockDim.x) {
+      const int t = i / n, j = i - t * n;
+      const double a = (double)p.pos[(int64_t)axis[j] * p.ldp + r0 + t] * turn[j];
+      float s, c;
+      sincospif(2.0f * (float)(a - rint(a)), &s, &c);
+      cs[i] = make_float2(c, s);
+    }
+    __syncthreads();
+    for (int i = tid; i < tt * units; i += blockDim.x) {
+      const int t = i / units;
+      int u = i - t * units;
+      const int64_t row = r0 + t;
+      const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+      if (u < u_rot) {
+        const int head = u / rot, j = (u - head * rot) * V;
+        T* out = head < p.nq ? static_cast<T*>(p.q) : static_cast<T*>(p.k);
+        if (out == nullptr) continue;
+        out += head < p.nq ? row * p.ldq + head * p.hd : row * p.ldk + (head - p.nq) * p.hd;
+        float lo[V], hi[V], a[V], b[V];
+        load_v<T, V>(x + head * p.hd + j, lo);
+        load_v<T, V>(x + head * p.hd + j + n, hi);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float2 w = cs[t * n + j + e];
+          a[e] = lo[e] * w.x - hi[e] * w.y;
+          b[e] = hi[e] * w.x + lo[e] * w.y;
+        }
+        store_v<T, V>(out + j, a);
+        store_v<T, V>(out + j + n, b);
+      } else {
+        u -= u_rot;
+        const T* src;
+        T* out;
+        if (u < u_tail) {
+          const int head = u / tail, e = 2 * n + (u - head * tail) * V;
+          out = head < p.nq ? static_cast<T*>(p.q) : static_cast<T*>(p.k);
+          if (out == nullptr) continue;
+          out += (head < p.nq ? row * p.ldq + head * p.hd : row * p.ldk + (head - p.nq) * p.hd) + e;
+          src = x + head * p.hd + e;
+        } else {
+          const int e = (u - u_tail) * V;
+          out = static_cast<T*>(p.v) + row * p.ldv + e;
+          src = x + heads * p.hd + e;
+        }
+        float w[V];
+        load_v<T, V>(src, w);
+        store_v<T, V>(out, w);
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_rope(RopeParams& p, bool wide, int sms, cudaStream_t st) {
+  const int v = wide ? 8 : 1;
+  const int units = ((p.nq + p.nkv) * (p.hd - p.n) + (p.v ? p.nkv * p.hd : 0)) / v;
+  int tt = 512 / (units > 0 ? units : 1);
+  tt = tt < 1 ? 1 : tt > 16 ? 16 : tt;
+  while (tt > 1 && (int64_t)p.rows < (int64_t)tt * sms * 4) tt >>= 1;   // few rows: spread them
+  p.tt = tt;
+  const int64_t tiles = ((int64_t)p.rows + tt - 1) / tt;
+  const int64_t most = (int64_t)sms * 8;
+  const unsigned grid = (unsigned)(tiles < most ? tiles : most);
+  const size_t smem = (size_t)tt * p.n * sizeof(float2);                // at most 16 KB
+  if (wide)
+    rope_kernel<T, 8><<<grid, 256, smem, st>>>(p);
+  else
+    rope_kernel<T, 1><<<grid, 256, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+bool mult16(const void* p, int64_t ld, size_t elem, int rows) {
+  return ((uintptr_t)p & 15u) == 0 && (rows <= 1 || ((uint64_t)ld * elem) % 16 == 0);
+}
+
+}  // namespace
+
+// ----------------------------------------------------------------- argument checks
+fm_status OpCheck::fail(fm_status st, const char* fmt, ...) {
+  char msg[320];
+  const int at = snprintf(msg, sizeof(msg), "%s: ", call);
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg + at, sizeof(msg) - at, fmt, ap);
+  va_end(ap);
+  set_thread_error(msg);
+  return st;
+}
+
+fm_status OpCheck::rows(const void* p, const char* name, int64_t ld, int64_t width, int n, size_t elem, size_t align) {
+  if (p == nullptr) return fail(FM_ERR_INVALID_ARG, "%s is NULL", name);
+  if (n > 1 && ld < width)
+    return fail(FM_ERR_INVALID_ARG, "%s: row stride %lld is below the row's %lld elements", name, (long long)ld,
+                (long long)width);
+  if (((uintptr_t)p % align) != 0 || (n > 1 && ((uint64_t)ld * elem) % align != 0))
+    return fail(FM_ERR_INVALID_ARG, "%s: rows must start on %d-byte boundaries", name, (int)align);
+  ptr[count] = p;
+  ptr_name[count++] = name;
+  return FM_OK;
+}
+
+fm_status OpCheck::memory() {
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(FM_ERR_CUDA, "no usable current CUDA device (%s)", cudaGetErrorString(e));
+  }
+  for (int i = 0; i < count; ++i) {
+    cudaPointerAttributes at;
+    e = cudaPointerGetAttributes(&at, ptr[i]);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return fail(FM_ERR_CUDA, "%s: cudaPointerGetAttributes: %s", ptr_name[i], cudaGetErrorString(e));
+    }
+    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged)
+      return fail(FM_ERR_INVALID_ARG, "%s is not device memory", ptr_name[i]);
+    if (at.type == cudaMemoryTypeDevice && at.device != device)
+      return fail(FM_ERR_INVALID_ARG, "%s is on device %d, the current device is %d", ptr_name[i], at.device, device);
+  }
+  return FM_OK;
+}
+
+fm_status OpCheck::launched(cudaError_t e) {
+  if (e == cudaSuccess) return FM_OK;
+  cudaGetLastError();
+  return fail(FM_ERR_CUDA, "%s", cudaGetErrorString(e));
+}
+
+int sm_count(int device) {
+  static std::atomic<int> known[64];
+  if (device >= 0 && device < 64) {
+    const int k = known[device].load(std::memory_order_relaxed);
+    if (k > 0) return k;
+  }
+  int n = 0;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = 148;
+  }
+  if (device >= 0 && device < 64) known[device].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+}  // namespace fm
+
+using fm::OpCheck;
+
+#define FM_TRY(expr)                   \
+  do {                                 \
+    const fm_status st_ = (expr);      \
+    if (st_ != FM_OK) return st_;      \
+  } while (0)
+
+extern "C" {
+#pragma GCC visibility push(default)
+
+fm_status fm_add_rmsnorm_e4m3(const void* x, fm_dtype x_type, int64_t ldx, const void* residual, fm_dtype h_type,
+                              int64_t ldr, const uint16_t* gain, float gain_offset, float eps, int rows, int d,
+                              void* h_out, int64_t ldh, uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
+                              void* stream) {
+  OpCheck c{"fm_add_rmsnorm_e4m3"};
+  fm::set_thread_error("");
+  if ((x_type != FM_BF16 && x_type != FM_F32) || (h_type != FM_BF16 && h_type != FM_F32))
+    return c.fail(FM_ERR_UNSUPPORTED, "x_type %d / h_type %d: FM_BF16 or FM_F32", (int)x_type, (int)h_type);
+  if (rows < 0 || d < 16 || d > 16384 || d % 16 != 0)
+    return c.fail(FM_ERR_INVALID_ARG, "rows %d / d %d out of range (d a multiple of 16, 16 .. 16384)", rows, d);
+  if (!(eps >= 0.f)) return c.fail(FM_ERR_INVALID_ARG, "eps must not be negative");
+  if (rows == 0) return FM_OK;
+  const size_t xs = x_type == FM_F32 ? 4 : 2, hs = h_type == FM_F32 ? 4 : 2;
+  FM_TRY(c.rows(x, "x", ldx, d, rows, xs, 16));
+  if (residual != nullptr) FM_TRY(c.rows(residual, "residual", ldr, d, rows, hs, 16));
+  if (gain != nullptr) FM_TRY(c.rows(gain, "gain", d, d, 1, 2, 16));
+  if (h_out != nullptr) FM_TRY(c.rows(h_out, "h_out", ldh, d, rows, hs, 16));
+  FM_TRY(c.rows(codes, "codes", ldc, d, rows, 1, 16));
+  FM_TRY(c.rows(scales, "scales", lds, (d + 127) / 128, rows, 4, 4));
+  FM_TRY(c.memory());
+  fm::NormParams p{x, residual, gain, h_out, codes, scales, ldx, ldr, ldh, ldc, lds, gain_offset, eps, rows, d, 0};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (x_type == FM_BF16)
+    return c.launched(h_type == FM_BF16 ? fm::launch_norm<uint16_t, uint16_t>(p, st)
+                                        : fm::launch_norm<uint16_t, float>(p, st));
+  return c.launched(h_type == FM_BF16 ? fm::launch_norm<float, uint16_t>(p, st) : fm::launch_norm<float, float>(p, st));
+}
+
+fm_status fm_gated_e4m3(const void* x, fm_dtype x_type, int64_t ldx, fm_act act, int rows, int f, uint8_t* codes,
+                        int64_t ldc, float* scales, int64_t lds, void* stream) {
+  OpCheck c{"fm_gated_e4m3"};
+  fm::set_thread_error("");
+  if (x_type != FM_BF16 && x_type != FM_F32)
+    return c.fail(FM_ERR_UNSUPPORTED, "x_type %d: FM_BF16 or FM_F32", (int)x_type);
+  if (act != FM_ACT_NONE && act != FM_ACT_SILU && act != FM_ACT_GELU_TANH)
+    return c.fail(FM_ERR_UNSUPPORTED, "act %d: FM_ACT_NONE, FM_ACT_SILU or FM_ACT_GELU_TANH", (int)act);
+  if (rows < 0 || f < 16 || f > (1 << 20) || f % 16 != 0)
+    return c.fail(FM_ERR_INVALID_ARG, "rows %d / f %d out of range (f a multiple of 16, 16 .. 2^20)", rows, f);
+  if ((int64_t)rows * ((f + 2047) / 2048) > 0x7FFFFFFF)
+    return c.fail(FM_ERR_INVALID_ARG, "rows %d x f %d is more than one launch takes", rows, f);
+  if (rows == 0) return FM_OK;
+  FM_TRY(c.rows(x, "x", ldx, act == FM_ACT_NONE ? f : 2 * (int64_t)f, rows, x_type == FM_F32 ? 4 : 2, 16));
+  FM_TRY(c.rows(codes, "codes", ldc, f, rows, 1, 16));
+  FM_TRY(c.rows(scales, "scales", lds, (f + 127) / 128, rows, 4, 4));
+  FM_TRY(c.memory());
+  fm::GatedParams p{x, codes, scales, ldx, ldc, lds, rows, f, 0, 0, 0};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return c.launched(x_type == FM_BF16 ? fm::launch_gated<uint16_t>(p, act, st) : fm::launch_gated<float>(p, act, st));
+}
+
+fm_status fm_quantize_weight_e4m3_b128(const uint16_t* w, int64_t ldw, int n, int k, uint8_t* codes, int64_t ldc,
+                                       float* scales, int64_t lds, void* stream) {
+  OpCheck c{"fm_quantize_weight_e4m3_b128"};
+  fm::set_thread_error("");
+  if (n < 0 || k < 0) return c.fail(FM_ERR_INVALID_ARG, "n %d / k %d negative", n, k);
+  if (n == 0 || k == 0) return FM_OK;
+  const int64_t gn = ((int64_t)n + 127) / 128, gk = ((int64_t)k + 127) / 128;
+  if (gn * gk > 0x7FFFFFFF) return c.fail(FM_ERR_INVALID_ARG, "n %d x k %d is more than one launch takes", n, k);
+  FM_TRY(c.rows(w, "w", ldw, k, n, 2, 2));
+  FM_TRY(c.rows(codes, "codes", ldc, k, n, 1, 1));
+  FM_TRY(c.rows(scales, "scales", lds, gk, (int)gn, 4, 4));
+  FM_TRY(c.memory());
+  fm::quantize_weight_kernel<<<(unsigned)(gn * gk), 256, 0, static_cast<cudaStream_t>(stream)>>>(w, ldw, n, k, codes, ldc,
+                                                                                               scales, lds);
+  return c.launched(cudaGetLastError());
+}
+
+fm_status fm_rope_axes(const void* x, fm_dtype type, int64_t ldx, int rows, int n_q, int n_kv, int head_dim,
+                       const int32_t* positions, int64_t ldp, int n_axes, const uint8_t* pair_axis,
+                       const double* pair_freq, int n_pairs, void* q_out, int64_t ldq, void* k_out, int64_t ldk,
+                       void* v_out, int64_t ldv, void* stream) {
+  OpCheck c{"fm_rope_axes"};
+  fm::set_thread_error("");
+  if (type != FM_BF16 && type != FM_F32) return c.fail(FM_ERR_UNSUPPORTED, "type %d: FM_BF16 or FM_F32", (int)type);
+  if (rows < 0 || n_q < 0 || n_kv < 0 || n_q > 1024 || n_kv > 1024)
+    return c.fail(FM_ERR_INVALID_ARG, "rows %d / n_q %d / n_kv %d out of range (0 .. 1024 heads)", rows, n_q, n_kv);
+  if (head_dim < 2 || head_dim > 256 || head_dim % 2 != 0 || n_pairs < 1 || n_pairs > head_dim / 2)
+    return c.fail(FM_ERR_INVALID_ARG, "head_dim %d / n_pairs %d out of range (head_dim even, 2 .. 256; 1 .. head_dim/2 pairs)",
+                  head_dim, n_pairs);
+  if (n_axes < 1 || n_axes > 8) return c.fail(FM_ERR_INVALID_ARG, "n_axes %d out of range (1 .. 8)", n_axes);
+  if (pair_axis == nullptr || pair_freq == nullptr)
+    return c.fail(FM_ERR_INVALID_ARG, "pair_axis and pair_freq must be host arrays, not NULL");
+  fm::RopeParams p;
+  for (int j = 0; j < n_pairs; ++j) {
+    if (pair_axis[j] >= n_axes)
+      return c.fail(FM_ERR_INVALID_ARG, "pair %d: axis %d of %d", j, (int)pair_axis[j], n_axes);
+    if (!std::isfinite(pair_freq[j])) return c.fail(FM_ERR_INVALID_ARG, "pair %d: frequency is not finite", j);
+    p.axis[j] = pair_axis[j];
+    p.turn[j] = pair_freq[j] * 0.15915494309189535;   // 1 / (2 pi)
+  }
+  for (int j = n_pairs; j < fm::kMaxPairs; ++j) {
+    p.axis[j] = 0;
+    p.turn[j] = 0.0;
+  }
+  if (n_q == 0) q_out = nullptr;
+  if (n_kv == 0) k_out = v_out = nullptr;
+  if (rows == 0 || (q_out == nullptr && k_out == nullptr && v_out == nullptr)) return FM_OK;
+  const size_t es = type == FM_F32 ? 4 : 2;
+  const int64_t wq = (int64_t)n_q * head_dim, wk = (int64_t)n_kv * head_dim;
+  FM_TRY(c.rows(x, "x", ldx, wq + (v_out != nullptr ? 2 : 1) * wk, rows, es, es));
+  FM_TRY(c.rows(positions, "positions", ldp, rows, n_axes, 4, 4));
+  if (q_out != nullptr) FM_TRY(c.rows(q_out, "q_out", ldq, wq, rows, es, es));
+  if (k_out != nullptr) FM_TRY(c.rows(k_out, "k_out", ldk, wk, rows, es, es));
+  if (v_out != nullptr) FM_TRY(c.rows(v_out, "v_out", ldv, wk, rows, es, es));
+  FM_TRY(c.memory());
+  p.x = x; p.pos = positions; p.q = q_out; p.k = k_out; p.v = v_out;
+  p.ldx = ldx; p.ldp = ldp; p.ldq = ldq; p.ldk = ldk; p.ldv = ldv;
+  p.rows = rows; p.nq = n_q; p.nkv = n_kv; p.hd = head_dim; p.n = n_pairs; p.tt = 1;
+  const bool wide = head_dim % 8 == 0 && n_pairs % 8 == 0 && fm::mult16(x, ldx, es, rows) &&
+                    fm::mult16(q_out, ldq, es, q_out ? rows : 0) && fm::mult16(k_out, ldk, es, k_out ? rows : 0) &&
+                    fm::mult16(v_out, ldv, es, v_out ? rows : 0);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int sms = fm::sm_count(c.device);
+  return c.launched(type == FM_BF16 ? fm::launch_rope<uint16_t>(p, wide, sms, st) : fm::launch_rope<float>(p, wide, sms, st));
+}
+
+#pragma GCC visibility pop
+}  // extern "C"
