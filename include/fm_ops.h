@@ -99,8 +99,8 @@ fm_status fm_quantize_weight_e4m3_b128(const uint16_t *w, int64_t ldw, int n, in
  * k: a multiple of 16, at least 16 (a and w rows on 16-byte boundaries); m
  * and n any.  sa, sw, bias and out need only their element's alignment.  The
  * result does not depend on anything but the operands (fixed summation
- * order).  A device-side wait that exceeds its bound leaves its tile
- * unwritten and is reported by fm_ops_sync. */
+ * order).  A device-side wait that exceeds its bound leaves its
+ * part of `out` unspecified and is reported by fm_ops_sync. */
 fm_status fm_gemm_e4m3_b128(const uint8_t *a, int64_t lda, const float *sa, int64_t ldsa,
                             const uint8_t *w, int64_t ldw, const float *sw, int64_t ldsw,
                             const uint16_t *bias, int m, int n, int k, void *out, fm_dtype out_type,

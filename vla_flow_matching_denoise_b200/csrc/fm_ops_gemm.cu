@@ -14,6 +14,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/fm_ops.h"
@@ -27,10 +28,6 @@ namespace {
 __device__ unsigned int g_ops_err;
 
 constexpr long long kSpin = 4000000000ll;       // ~2 s of SM cycles
-constexpr int kStages = 5;
-constexpr int kTileA = 128 * 128, kTileW = 128 * 128, kStage = kTileA + kTileW;
-constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 256;
-constexpr int kThreads = 192;
 
 struct GemmParams {
   const float *sa, *sw;
@@ -40,7 +37,7 @@ struct GemmParams {
   int m, n, groups, f32;
 };
 
-// 2-D tiled load of a [128 rows][128 bytes] box at (column c0, row c1).
+// 2-D tiled load of a box of 128-byte rows at (column c0, row c1).
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int c0, int c1, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -48,21 +45,76 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int 
       "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// (c0, c1) += (a0, a1) * (b0, b1): one instruction for two fp32 FMAs.
+__device__ __forceinline__ void fma2(float& c0, float& c1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%0, %1};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "+f"(c0), "+f"(c1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+__device__ __forceinline__ void store_out(const GemmParams& p, int i, int j, float v) {
+  if (p.f32)
+    static_cast<float*>(p.out)[(int64_t)i * p.ldo + j] = v;
+  else
+    static_cast<__nv_bfloat16*>(p.out)[(int64_t)i * p.ldo + j] = __float2bfloat16_rn(v);
+}
 
-__global__ void __launch_bounds__(kThreads, 1)
-gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw,
-            const __grid_constant__ GemmParams p) {
+// ----------------------------------------------------------------- few rows
+// The weights are the 128-row operand and BT rows of `a` the narrow one, so a
+// single row costs the tensor cores 16 columns and not 128; thread = output
+// channel, so a warp stores 32 consecutive channels of a row.  The blocks of
+// a cluster split the groups of k (there are too few tiles to fill the GPU
+// and the time is that of streaming the weights), leave their sums in shared
+// memory and each adds a share of the rows over all of them in rank order.
+constexpr int kAhead = 8;      // groups of scales brought to shared memory at a time
+
+template <int BT>
+struct Narrow {
+  static constexpr int kW = 128 * 128, kStage = kW + BT * 128;
+  static constexpr int kStages = BT == 128 ? 6 : BT == 64 ? 4 : 5;
+  static constexpr int kThreads = 192;
+  static constexpr int kScales = 2 * kAhead * BT * 4;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kScales + 256;
+  static_assert((size_t)kStages * kStage >= (size_t)BT * 128 * 4, "the sums reuse the ring");
+};
+
+template <int BT>
+__global__ void __launch_bounds__(192, 1)
+narrow_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw,
+              const __grid_constant__ GemmParams p, int split) {
+  using C = Narrow<BT>;
   extern __shared__ uint8_t raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)kStages * kStage);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;     // [2]
+  uint8_t* ring = align1024(raw);
+  float* scales = reinterpret_cast<float*>(ring + (size_t)C::kStages * C::kStage);   // [2][kAhead][BT]
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(scales) + C::kScales);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tfull = empty + C::kStages;  // [2]
   uint64_t* tempty = tfull + 2;          // [2]
   uint64_t* drain = tempty + 2;
   uint32_t* slot = reinterpret_cast<uint32_t*>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
@@ -73,110 +125,590 @@ gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     mbar_init(smem_u32(drain), 1);
     fence_mbar_init();
   }
+  constexpr int kCols = 2 * BT;          // a power of two, at least 32
   if (warp == 1) {
-    tmem_alloc(smem_u32(slot), 256);
+    tmem_alloc(smem_u32(slot), kCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const unsigned mt = (unsigned)((p.m + 127) / 128);
-  const int m0 = (int)(blockIdx.x % mt) * 128, n0 = (int)(blockIdx.x / mt) * 128;
+  const unsigned rank = split > 1 ? cluster_rank() : 0, tile = blockIdx.x / (unsigned)split;
+  const unsigned rt = (unsigned)((p.m + BT - 1) / BT);
+  const int i0 = (int)(tile % rt) * BT, nb = (int)(tile / rt), n0 = nb * 128;
+  const int g0 = (int)((int64_t)p.groups * rank / split), g1 = (int)((int64_t)p.groups * (rank + 1) / split);
+  const int count = g1 - g0;
 
   if (warp == 0) {
     if (lane == 0) {
       int it = 0;
-      for (; it < p.groups; ++it) {
-        const int s = it % kStages;
-        if (it >= kStages && !mbar_wait(smem_u32(&empty[s]), ((it / kStages) & 1) ^ 1, kSpin)) {
+      for (; it < count; ++it) {
+        const int s = it % C::kStages;
+        if (it >= C::kStages && !mbar_wait(smem_u32(&empty[s]), ((it / C::kStages) & 1) ^ 1, kSpin)) {
           atomicOr(&g_ops_err, 1u);
           break;
         }
-        const uint32_t dst = smem_u32(ring + (size_t)s * kStage), bar = smem_u32(&full[s]);
-        mbar_arrive_expect_tx(bar, kStage);
-        tma_load_2d(dst, &ma, it * 128, m0, bar);
-        tma_load_2d(dst + kTileA, &mw, it * 128, n0, bar);
+        const uint32_t dst = smem_u32(ring + (size_t)s * C::kStage), bar = smem_u32(&full[s]);
+        mbar_arrive_expect_tx(bar, C::kStage);
+        tma_load_2d(dst, &mw, (g0 + it) * 128, n0, bar);
+        tma_load_2d(dst + C::kW, &ma, (g0 + it) * 128, i0, bar);
       }
-      // every issued copy lands before the block may exit
-      for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
-        mbar_wait(smem_u32(&full[j % kStages]), (j / kStages) & 1, kSpin);
+      // every issued copy lands before its memory is used for anything else
+      for (int j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
+        mbar_wait(smem_u32(&full[j % C::kStages]), (j / C::kStages) & 1, kSpin);
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(128, 128);
-      for (int it = 0; it < p.groups; ++it) {
-        const int s = it % kStages, b = it & 1;
+      constexpr uint32_t idesc = idesc_e4m3(128, BT);
+      for (int it = 0; it < count; ++it) {
+        const int s = it % C::kStages, b = it & 1;
         if ((it >= 2 && !mbar_wait(smem_u32(&tempty[b]), ((it >> 1) - 1) & 1, kSpin)) ||
-            !mbar_wait(smem_u32(&full[s]), (it / kStages) & 1, kSpin)) {
+            !mbar_wait(smem_u32(&full[s]), (it / C::kStages) & 1, kSpin)) {
           atomicOr(&g_ops_err, 2u);
           break;
         }
         tc_fence_after();
-        const uint32_t a = smem_u32(ring + (size_t)s * kStage);
+        const uint32_t w = smem_u32(ring + (size_t)s * C::kStage);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          mma_e4m3(tmem + b * 128, desc_sw128(a + j * 32), desc_sw128(a + kTileA + j * 32), idesc, j != 0);
+          mma_e4m3(tmem + b * BT, desc_sw128(w + j * 32), desc_sw128(w + C::kW + j * 32), idesc, j != 0);
         mma_commit(smem_u32(&empty[s]));
         mma_commit(smem_u32(&tfull[b]));
       }
-      mma_commit(smem_u32(drain));             // every MMA is done before TMEM is released
+      mma_commit(smem_u32(drain));             // every MMA is done before TMEM and the ring are given up
       mbar_wait(smem_u32(drain), 0, kSpin);
     }
   } else {
-    const int row = 32 * (warp & 3) + lane;    // TMEM lane
-    const int i = m0 + row;
-    const bool valid = i < p.m;
+    const int et = threadIdx.x - 64;           // 0 .. 127
+    const int row = 32 * (warp & 3) + lane;    // TMEM lane: output channel n0 + row
     const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const float* sa = p.sa + (int64_t)i * p.ldsa;
-    const float* sw = p.sw + (int64_t)(n0 >> 7) * p.ldsw;
-    float acc[128];
+    const float* sw = p.sw + (int64_t)nb * p.ldsw + g0;
+    // Scales of kAhead groups: this thread brings row i0 + st, groups sg, sg + kPer, ...
+    constexpr int kPer = 128 / BT;
+    constexpr int kMine = kAhead / kPer > 0 ? kAhead / kPer : 1;
+    const int st = et % BT, sg = et / BT;
+    const bool srow = i0 + st < p.m && sg < kAhead;
+    const float* sa = p.sa + (int64_t)(i0 + st) * p.ldsa + g0;
+    float next[kMine];
+    auto fetch = [&](int base) {
 #pragma unroll
-    for (int c = 0; c < 128; ++c) acc[c] = 0.f;
+      for (int q = 0; q < kMine; ++q) {
+        const int g = base + sg + q * kPer;
+        next[q] = srow && g < count ? sa[g] * sw[g] : 0.f;
+      }
+    };
+    auto keep = [&](int buf) {
+#pragma unroll
+      for (int q = 0; q < kMine; ++q)
+        if (sg + q * kPer < kAhead) scales[(buf * kAhead + sg + q * kPer) * BT + st] = next[q];
+    };
+    float acc[BT];
+#pragma unroll
+    for (int c = 0; c < BT; ++c) acc[c] = 0.f;
     bool ok = true;
-    for (int it = 0; it < p.groups; ++it) {
-      const int b = it & 1;
-      const float s = valid ? sa[it] * sw[it] : 0.f;
-      // every lane of the warp gets the same answer: the barrier is shared
+    fetch(0);
+    for (int it = 0; it < count; ++it) {
+      const int b = it & 1, sb = (it / kAhead) & 1;
+      if (it % kAhead == 0) {
+        keep(sb);
+        named_bar_sync(1, 128);
+        fetch(it + kAhead);
+      }
+      if (!ok) continue;                       // after a timeout: only the barrier, which the warps share
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tfull[b]), (it >> 1) & 1, kSpin));
       if (!ok) {
         if (lane == 0) atomicOr(&g_ops_err, 4u);
-        break;
+        continue;
       }
       tc_fence_after();
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
+      const float* s = scales + (sb * kAhead + it % kAhead) * BT;
+      if constexpr (BT == 16) {
         float v[16];
-        tmem_ld16(ta + b * 128 + q * 16, v);
+        tmem_ld16(ta + b * BT, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[q * 16 + e] = fmaf(v[e], s, acc[q * 16 + e]);
+        for (int e = 0; e < 16; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(s + e);
+          fma2(acc[e], acc[e + 1], v[e], v[e + 1], f.x, f.y);
+          fma2(acc[e + 2], acc[e + 3], v[e + 2], v[e + 3], f.z, f.w);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < BT / 32; ++q) {
+          float v[32];
+          tmem_ld32(ta + b * BT + q * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(s + q * 32 + e);
+            float* a = acc + q * 32 + e;
+            fma2(a[0], a[1], v[e], v[e + 1], f.x, f.y);
+            fma2(a[2], a[3], v[e + 2], v[e + 3], f.z, f.w);
+          }
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tempty[b]));
     }
-    if (ok && valid) {
+    const int rows = p.m - i0 < BT ? p.m - i0 : BT;
+    if (split == 1) {
+      const int j = n0 + row;
+      if (ok && j < p.n) {
+        const float bias = p.bias != nullptr ? __uint_as_float((uint32_t)p.bias[j] << 16) : 0.f;
 #pragma unroll
-      for (int c = 0; c < 128; ++c) {
-        const int j = n0 + c;
-        if (j < p.n) {
-          float v = acc[c];
-          if (p.bias != nullptr) v += __uint_as_float((uint32_t)p.bias[j] << 16);
-          if (p.f32)
-            static_cast<float*>(p.out)[(int64_t)i * p.ldo + j] = v;
-          else
-            static_cast<__nv_bfloat16*>(p.out)[(int64_t)i * p.ldo + j] = __float2bfloat16_rn(v);
-        }
+        for (int c = 0; c < BT; ++c)
+          if (c < rows) store_out(p, i0 + c, j, acc[c] + bias);
+      }
+    } else {
+      // the ring is free: every MMA that reads it has completed (the last tfull)
+      float* part = reinterpret_cast<float*>(ring);          // [BT][128]
+#pragma unroll
+      for (int c = 0; c < BT; ++c)
+        if (c < rows) part[c * 128 + row] = acc[c];
+    }
+  }
+  __syncwarp();
+  if (split > 1) {
+    cluster_sync_all();
+    if (warp >= 2) {
+      const int rows = p.m - i0 < BT ? p.m - i0 : BT;
+      const int c0 = rows * (int)rank / split, c1 = rows * ((int)rank + 1) / split;
+      const int row = threadIdx.x - 64, j = n0 + row;
+      const float bias = j < p.n && p.bias != nullptr ? __uint_as_float((uint32_t)p.bias[j] << 16) : 0.f;
+      for (int c = c0; c < c1; ++c) {
+        const uint32_t at = smem_u32(reinterpret_cast<float*>(ring) + c * 128 + row);
+        float v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < split) v[r] = ld_dsmem_f1(map_shared_rank(at, r));
+        float sum = v[0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (r < split) sum += v[r];
+        if (j < p.n) store_out(p, i0 + c, j, sum + bias);
       }
     }
+    cluster_sync_all();                        // no block leaves while another reads its sums
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, kCols);
   }
+}
+
+template <int BT>
+cudaError_t launch_narrow(const CUtensorMap& ma, const CUtensorMap& mw, const GemmParams& p, int split, cudaStream_t st) {
+  using C = Narrow<BT>;
+  cudaError_t e = cudaFuncSetAttribute(narrow_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (((int64_t)p.m + BT - 1) / BT) * (((int64_t)p.n + 127) / 128);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, narrow_kernel<BT>, ma, mw, p, split);
+}
+
+// ----------------------------------------------------------------- many rows
+// A pair of blocks (cluster of 2, cta_group::2) owns a tile of 256 rows of `a`
+// x 256 output channels: each block brings its own 128 rows and half of the
+// weights (32 KB a group for 128 x 256 x 128 products), which halves the
+// operand traffic a 128 x 256 tile of one block would need.  The leader issues
+// M = 256, N = 128 products, one half of the channels after the other, into
+// two TMEM accumulators per half; four epilogue warps per half and block
+// scale and sum them, thread = row, so a group's factor is one register.  Half
+// the channels at a time, because an accumulator is given back ~500 cycles after
+// its products end (commit, read, arrive across the pair), as long as the 512
+// cycles a whole group takes: with halves three units are in flight meanwhile.
+// Outputs leave through shared memory, by TMA where `out` allows it.
+struct Wide {
+  static constexpr int kA = 128 * 128, kB = 64 * 128, kStage = kA + 2 * kB;
+  static constexpr int kStages = 5;
+  static constexpr int kSlot = 4096;               // 32 rows x 128 bytes of output
+  static constexpr int kThreads = 384;             // 8 epilogue warps, TMA, 2 x MMA, one idle
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 16 * kSlot + 2 * 256 * 2 + 256;
+  static_assert(kSmem <= 232448, "227 KB");
+};
+
+__device__ __forceinline__ uint32_t leader_addr(uint32_t a) { return map_shared_rank(a, 0); }
+// As tma_load_2d, completing on a barrier of the pair (shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int c0, int c1, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(tmap), "r"(c0),
+               "r"(c1), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+template <int ACC>
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "n"(ACC)
+      : "memory");
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Arrives on `bar` of both blocks of the pair when this thread's MMAs are done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar)
+      : "memory");
+}
+// Relaxed: what it hands over is a TMEM accumulator whose loads have returned
+// (tcgen05.wait::ld), no memory; a release of cluster scope waits for all the
+// thread's memory operations and cost ~1000 cycles a group (956 -> 490 us at
+// 8192^3).
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// Tiles in bands of 8 row tiles, so that the tiles in flight share operands in L2.
+struct TileAt {
+  int mt, nt;
+};
+__device__ __forceinline__ TileAt tile_at(unsigned t, unsigned mts, unsigned nts) {
+  const unsigned band = t / (8 * nts), r = t - band * 8 * nts;
+  const unsigned h = mts - band * 8 < 8 ? mts - band * 8 : 8;
+  return TileAt{(int)(band * 8 + r % h), (int)(r / h)};
+}
+
+// 4 consecutive scales from group g on (0 past the last); `v4`: 16-byte loads allowed.
+__device__ __forceinline__ float4 scales4(const float* s, int g, int groups, bool v4) {
+  if (v4 && g + 4 <= groups) return *reinterpret_cast<const float4*>(s + g);
+  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (g < groups) r.x = s[g];
+  if (g + 1 < groups) r.y = s[g + 1];
+  if (g + 2 < groups) r.z = s[g + 2];
+  if (g + 3 < groups) r.w = s[g + 3];
+  return r;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
+wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw,
+            const __grid_constant__ CUtensorMap mo, const __grid_constant__ GemmParams p, int tma_out) {
+  using C = Wide;
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = align1024(raw);
+  uint8_t* slots = ring + (size_t)C::kStages * C::kStage;
+  uint16_t* bias_s = reinterpret_cast<uint16_t*>(slots + 16 * C::kSlot);   // [2][256]
+  uint64_t* full = reinterpret_cast<uint64_t*>(bias_s + 512);          // the leader's
+  uint64_t* empty = full + C::kStages;
+  uint64_t* tfull = empty + C::kStages;      // [half][buffer]
+  uint64_t* tempty = tfull + 4;              // [half][buffer], the leader's
+  uint64_t* drain = tempty + 4;              // [half]
+  uint32_t* slot = reinterpret_cast<uint32_t*>(drain + 2);
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 2);
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(smem_u32(&tfull[b]), 1);
+      mbar_init(smem_u32(&tempty[b]), 8);
+    }
+    mbar_init(smem_u32(&drain[0]), 1);
+    mbar_init(smem_u32(&drain[1]), 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();                        // both blocks' barriers exist before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  const unsigned mts = (unsigned)((p.m + 255) / 256), nts = (unsigned)((p.n + 255) / 256);
+  const unsigned tiles = mts * nts, pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
+
+  // 384 threads start with 168 registers: 4 warps keep 40, 8 get 232 (64512 in all)
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 8) {
+      const uint32_t empty0 = smem_u32(empty), full0 = smem_u32(full), ring0 = smem_u32(ring), lead0 = leader_addr(full0);
+      uint32_t it = 0, s = 0, ph = 1;        // a fresh barrier's previous phase counts as done
+      bool ok = true;
+      for (unsigned t = first; ok && t < tiles; t += pairs) {
+        const TileAt at = tile_at(t, mts, nts);
+        const int m0 = at.mt * 256 + (int)rank * 128, n0 = at.nt * 256 + (int)rank * 64;
+        for (int g = 0; g < p.groups; ++g, ++it) {
+          ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ph, kSpin));
+          if (!ok) {
+            if (lane == 0) atomicOr(&g_ops_err, 8u);
+            break;
+          }
+          if (elect_one()) {
+            const uint32_t dst = ring0 + s * C::kStage, bar = lead0 + 8 * s;
+            if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * C::kStage);
+            tma_load_2d_pair(dst, &ma, g * 128, m0, bar);
+            tma_load_2d_pair(dst + C::kA, &mw, g * 128, n0, bar);
+            tma_load_2d_pair(dst + C::kA + C::kB, &mw, g * 128, n0 + 128, bar);
+          }
+          __syncwarp();
+          if (++s == C::kStages) s = 0, ph ^= 1;
+        }
+      }
+      // the leader sees both blocks' copies land before either may exit
+      if (rank == 0)
+        for (uint32_t j = it > (uint32_t)C::kStages ? it - C::kStages : 0; j < it; ++j)
+          mbar_wait(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1, kSpin);
+    } else if (warp < 11 && rank == 0) {
+      // The whole warp runs the loop and one elected lane issues, so that the
+      // descriptors live in uniform registers: a lone thread spent ~1000 cycles
+      // a group on building and moving them, twice the products' time.
+      constexpr uint32_t idesc = idesc_e4m3(256, 128);
+      const uint32_t h = warp - 9;
+      const uint64_t d0 = desc_sw128(smem_u32(ring)), w0 = desc_sw128(smem_u32(ring) + C::kA + h * C::kB);
+      const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), tfull0 = smem_u32(tfull + 2 * h),
+                     tempty0 = smem_u32(tempty + 2 * h), dst0 = tmem + h * 256;
+      uint32_t s = 0, ph = 0, b = 0, bph = 1;
+      bool ok = true;
+      for (unsigned t = first; ok && t < tiles; t += pairs) {
+        for (int g = 0; g < p.groups; ++g) {
+          ok = __all_sync(0xffffffffu, mbar_wait(tempty0 + 8 * b, bph, kSpin) && mbar_wait(full0 + 8 * s, ph, kSpin));
+          if (!ok) {
+            if (lane == 0) atomicOr(&g_ops_err, 16u);
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t d = dst0 + b * 128;
+            const uint64_t ad = d0 + s * (C::kStage >> 4), bd = w0 + s * (C::kStage >> 4);
+            mma_e4m3_pair<0>(d, ad, bd, idesc);
+            mma_e4m3_pair<1>(d, ad + 2, bd + 2, idesc);
+            mma_e4m3_pair<1>(d, ad + 4, bd + 4, idesc);
+            mma_e4m3_pair<1>(d, ad + 6, bd + 6, idesc);
+            mma_commit_pair(tfull0 + 8 * b);
+            mma_commit_pair(empty0 + 8 * s);
+          }
+          __syncwarp();
+          if (++s == C::kStages) s = 0, ph ^= 1;
+          if ((b ^= 1) == 0) bph ^= 1;
+        }
+      }
+      if (elect_one())
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain + h))
+                     : "memory");
+      __syncwarp();
+      mbar_wait(smem_u32(drain + h), 0, kSpin);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int q4 = warp & 3, h = warp >> 2;
+    const uint32_t ta = tmem + ((uint32_t)(32 * q4) << 16) + h * 256;
+    const uint32_t te0 = leader_addr(smem_u32(&tempty[2 * h])), te1 = leader_addr(smem_u32(&tempty[2 * h + 1]));
+    uint8_t* stage = slots + warp * 2 * C::kSlot;
+    const bool v4 = (reinterpret_cast<uintptr_t>(p.sa) & 15) == 0 && p.ldsa % 4 == 0;
+    int b = 0, bph = 0, par = 0;
+    bool ok = true;
+    // This row's scales: four groups in hand and four on the way, and the next
+    // channel scale; a tile's first ones are fetched before the tile ahead of it
+    // is written out.
+    float4 fa, fn;
+    float wn;
+    const float *sa, *sw;
+    int m0, n0;
+    auto enter = [&](unsigned t) {
+      const TileAt at = tile_at(t, mts, nts);
+      m0 = at.mt * 256 + (int)rank * 128 + 32 * q4;
+      n0 = at.nt * 256 + h * 128;
+      const bool live = m0 + lane < p.m && n0 < p.n;
+      sa = p.sa + (int64_t)(live ? m0 + lane : 0) * p.ldsa;
+      sw = p.sw + (int64_t)(live ? n0 >> 7 : 0) * p.ldsw;
+      fa = scales4(sa, 0, p.groups, v4);
+      fn = scales4(sa, 4, p.groups, v4);
+      wn = sw[0];
+    };
+    if (first < tiles) enter(first);
+    for (unsigned t = first; t < tiles; t += pairs, par ^= 1) {
+      float acc[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) acc[c] = 0.f;
+      for (int g = 0; g < p.groups; ++g) {
+        const float s = fa.x * wn;
+        if (g + 1 < p.groups) wn = sw[g + 1];
+        if ((g & 3) == 3) {
+          fa = fn;
+          fn = scales4(sa, g + 5, p.groups, v4);
+        } else {
+          fa.x = fa.y;
+          fa.y = fa.z;
+          fa.z = fa.w;
+        }
+        if (!ok) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tfull[2 * h + b]), bph, kSpin));
+        if (!ok) {
+          if (lane == 0) atomicOr(&g_ops_err, 32u);
+          continue;
+        }
+        tc_fence_after();
+        float v[2][16];
+        tmem_ld16(ta + b * 128, v[0]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          tmem_ld_wait();
+          if (q < 7) {
+            tmem_ld16(ta + b * 128 + (q + 1) * 16, v[(q + 1) & 1]);
+          } else {                               // all read: the accumulator goes back before the last sums
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(b ? te1 : te0);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            fma2(acc[q * 16 + e], acc[q * 16 + e + 1], v[q & 1][e], v[q & 1][e + 1], s, s);
+        }
+        if ((b ^= 1) == 0) bph ^= 1;
+      }
+      const int row0 = m0, col0 = n0;
+      if (t + pairs < tiles) enter(t + pairs);
+      if (p.bias != nullptr) {
+        const int j = col0 + 32 * q4 + lane;
+        uint16_t* bs = bias_s + par * 256 + h * 128;
+        bs[32 * q4 + lane] = j < p.n ? p.bias[j] : 0;
+        named_bar_sync(1 + h, 128);
+#pragma unroll
+        for (int c = 0; c < 128; c += 2) {
+          const uint32_t f = *reinterpret_cast<const uint32_t*>(bs + c);
+          acc[c] += __uint_as_float(f << 16);
+          acc[c + 1] += __uint_as_float(f & 0xFFFF0000u);
+        }
+      }
+      // the warp's rows, 128 bytes of them at a time (64 bf16 or 32 fp32
+      // columns), as 16-byte pieces swizzled by (row & 7)
+      const int sw7 = lane & 7;
+      auto flush = [&](int half, int c0, int width) {      // slot `half` holds columns c0 .. c0 + width - 1
+        if (tma_out) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && ok && row0 < p.m && c0 < p.n) {
+            tma_store_2d(&mo, c0, row0, smem_u32(stage + half * C::kSlot));
+          }
+          if (lane == 0) bulk_commit_group();
+        } else {
+          __syncwarp();
+          const int per = width / 32;                      // 2 bf16 or 1 fp32 per lane and row
+          for (int r = 0; r < 32 && row0 + r < p.m && ok; ++r) {
+            const uint32_t word = *reinterpret_cast<const uint32_t*>(stage + half * C::kSlot + r * 128 +
+                                                                     (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+            const int j = c0 + lane * per;
+            if (per == 1) {
+              if (j < p.n) static_cast<float*>(p.out)[(int64_t)(row0 + r) * p.ldo + j] = __uint_as_float(word);
+            } else {
+              uint16_t* o = static_cast<uint16_t*>(p.out) + (int64_t)(row0 + r) * p.ldo + j;
+              if (j < p.n) o[0] = (uint16_t)word;
+              if (j + 1 < p.n) o[1] = (uint16_t)(word >> 16);
+            }
+          }
+          __syncwarp();
+        }
+      };
+      if (tma_out && lane == 0) bulk_wait_read();          // the previous tile's slots have been read
+      __syncwarp();
+      if (p.f32) {
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
+          if (part == 2) {
+            if (tma_out && lane == 0) bulk_wait_read();
+            __syncwarp();
+          }
+          uint8_t* o = stage + (part & 1) * C::kSlot + lane * 128;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float* a = acc + part * 32 + k * 4;
+            *reinterpret_cast<float4*>(o + ((k ^ sw7) << 4)) = make_float4(a[0], a[1], a[2], a[3]);
+          }
+          flush(part & 1, col0 + part * 32, 32);
+        }
+      } else {
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint8_t* o = stage + part * C::kSlot + lane * 128;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float* a = acc + part * 64 + k * 8;
+            *reinterpret_cast<uint4*>(o + ((k ^ sw7) << 4)) =
+                make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
+          }
+          flush(part, col0 + part * 64, 64);
+        }
+      }
+    }
+    if (tma_out && lane == 0) bulk_wait_all();
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// Pairs of blocks that can run at once on the current device.
+int wide_pairs(int device) {
+  static std::atomic<int> known[64];
+  if (device >= 0 && device < 64) {
+    const int k = known[device].load(std::memory_order_relaxed);
+    if (k > 0) return k;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(148);
+  cfg.blockDim = dim3(Wide::kThreads);
+  cfg.dynamicSmemBytes = Wide::kSmem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, wide_kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = sm_count(device) / 2;
+  }
+  if (device >= 0 && device < 64) known[device].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+cudaError_t launch_wide(const CUtensorMap& ma, const CUtensorMap& mw, const CUtensorMap& mo, const GemmParams& p,
+                        bool tma_out, int device, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Wide::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (((int64_t)p.m + 255) / 256) * (((int64_t)p.n + 255) / 256);
+  const int pairs = wide_pairs(device);
+  const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
+  wide_kernel<<<grid, Wide::kThreads, Wide::kSmem, st>>>(ma, mw, mo, p, tma_out ? 1 : 0);
+  return cudaGetLastError();
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -210,6 +742,20 @@ bool codes_map(CUtensorMap* map, const uint8_t* p, int64_t ld, int rows, int k, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// `out` as boxes of 32 rows x 128 bytes, SW128; false where TMA cannot address it.
+bool out_map(CUtensorMap* map, void* p, int64_t ldo, int m, int n, bool f32) {
+  const EncodeFn fn = encode_fn();
+  const size_t es = f32 ? 4 : 2;
+  if (fn == nullptr || ((uintptr_t)p & 15) != 0 || (m > 1 && ((uint64_t)ldo * es) % 16 != 0)) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)n, (cuuint64_t)m};
+  const cuuint64_t strides[1] = {m > 1 ? (cuuint64_t)ldo * es : (((cuuint64_t)n * es + 15) & ~(cuuint64_t)15)};
+  const cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
+  const cuuint32_t one[2] = {1, 1};
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 }  // namespace fm
 
@@ -235,7 +781,7 @@ fm_status fm_gemm_e4m3_b128(const uint8_t* a, int64_t lda, const float* sa, int6
     return c.fail(FM_ERR_INVALID_ARG, "m %d / n %d / k %d out of range (k a positive multiple of 16)", m, n, k);
   if (m == 0 || n == 0) return FM_OK;
   const int64_t groups = ((int64_t)k + 127) / 128, tiles = (((int64_t)m + 127) / 128) * (((int64_t)n + 127) / 128);
-  if (tiles > 0x7FFFFFFF || n > 0x7FFFFF00 || m > 0x7FFFFF00 || k > 0x7FFFFF00)
+  if (tiles > 0x0FFFFFFF || n > 0x7FFFFF00 || m > 0x7FFFFF00 || k > 0x7FFFFF00)
     return c.fail(FM_ERR_INVALID_ARG, "m %d x n %d x k %d is more than one launch takes", m, n, k);
   FM_TRY(c.rows(a, "a", lda, k, m, 1, 16));
   FM_TRY(c.rows(sa, "sa", ldsa, groups, m, 4, 4));
@@ -244,14 +790,29 @@ fm_status fm_gemm_e4m3_b128(const uint8_t* a, int64_t lda, const float* sa, int6
   if (bias != nullptr) FM_TRY(c.rows(bias, "bias", n, n, 1, 2, 2));
   FM_TRY(c.rows(out, "out", ldo, n, m, out_type == FM_F32 ? 4 : 2, out_type == FM_F32 ? 4 : 2));
   FM_TRY(c.memory());
-  CUtensorMap ma, mw;
-  if (!fm::codes_map(&ma, a, lda, m, k, 128) || !fm::codes_map(&mw, w, ldw, n, k, 128))
+  const int sms = fm::sm_count(c.device);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const fm::GemmParams p{sa, sw, bias, out, ldsa, ldsw, ldo, m, n, (int)groups, out_type == FM_F32};
+  const bool wide = m > 256 && (int64_t)m * n >= 256 * 256 * 24;
+  int bt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+  int split = 1;
+  if (!wide) {
+    const int64_t few = (((int64_t)m + bt - 1) / bt) * (((int64_t)n + 127) / 128);
+    while (split < 8 && split * 2 <= groups && few * split * 2 <= sms * (bt <= 64 ? 2 : 1)) split *= 2;
+  }
+  CUtensorMap ma, mw, mo;
+  if (!fm::codes_map(&ma, a, lda, m, k, wide ? 128 : bt) || !fm::codes_map(&mw, w, ldw, n, k, wide ? 64 : 128))
     return c.fail(FM_ERR_CUDA, "the tensor maps of a and w were refused (m %d, n %d, k %d, strides %lld, %lld)", m, n, k,
                   (long long)lda, (long long)ldw);
-  FM_TRY(c.launched(cudaFuncSetAttribute(fm::gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fm::kSmem)));
-  fm::GemmParams p{sa, sw, bias, out, ldsa, ldsw, ldo, m, n, (int)groups, out_type == FM_F32};
-  fm::gemm_kernel<<<(unsigned)tiles, fm::kThreads, fm::kSmem, static_cast<cudaStream_t>(stream)>>>(ma, mw, p);
-  return c.launched(cudaGetLastError());
+  if (wide) {
+    const bool tma_out = fm::out_map(&mo, out, ldo, m, n, out_type == FM_F32);
+    if (!tma_out) mo = ma;
+    return c.launched(fm::launch_wide(ma, mw, mo, p, tma_out, c.device, st));
+  }
+  return c.launched(bt == 16   ? fm::launch_narrow<16>(ma, mw, p, split, st)
+                    : bt == 32 ? fm::launch_narrow<32>(ma, mw, p, split, st)
+                    : bt == 64 ? fm::launch_narrow<64>(ma, mw, p, split, st)
+                               : fm::launch_narrow<128>(ma, mw, p, split, st));
 }
 
 fm_status fm_ops_sync(void* stream) {
