@@ -635,3 +635,17 @@ def test_backbone_prefix_into_the_expert():
     ref = O.denoise(x0, 10, raw, [bits(k) for k in ks], [bits(v) for v in vs], s)
     cos = float(np.dot(out.ravel(), ref.ravel()) / (np.linalg.norm(out) * np.linalg.norm(ref)))
     assert cos >= 0.999 and np.max(np.abs(out - ref)) <= 5e-2      # the library's own bars of this workload
+
+
+def test_given_stream():
+    """`stream` as a torch stream or a handle: work and new outputs belong to it."""
+    ins = _layer_inputs(70, 5)
+    _, a, sa = ops.add_rmsnorm_e4m3(ins["x"], ins["gain"], residual=ins["h"])
+    want = ops.gemm_e4m3(a, sa, *ins["wq"])
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s in (st, st.cuda_stream):
+        _, a2, sa2 = ops.add_rmsnorm_e4m3(ins["x"], ins["gain"], residual=ins["h"], stream=s)
+        got = ops.gemm_e4m3(a2, sa2, *ins["wq"], stream=s)
+        ops.sync(s)
+        assert torch.equal(got, want)

@@ -3,7 +3,9 @@
     python -m vla_flow_matching_denoise_b200.build [--force]
 
 Output: vla_flow_matching_denoise_b200/libfm_expert.so (C ABI declared in
-include/fm_expert.h).  Rebuilds only when a source is newer than the library.
+include/fm_expert.h and include/fm_ops.h) and _ops.so beside it (the Python
+module that calls include/fm_ops.h on torch tensors; host code only, linked to
+the library).  Rebuilds only what is older than its sources.
 """
 from __future__ import annotations
 
@@ -11,11 +13,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfm_expert.so")
+OPS = os.path.join(PKG, "_ops.so")
 SOURCES = ["fm_api.cu", "fm_prep.cu", "fm_time.cu", "fm_step.cu", "fm_batch.cu", "fm_attn.cu", "fm_noalloc.cu",
            "fm_ops.cu", "fm_ops_gemm.cu"]
 HEADERS = ["fm_internal.h", "fm_batch.h", "fm_launch.h", "fm_ptx.cuh", "fm_ops_check.h"]
@@ -39,7 +43,35 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _build_ops(force: bool) -> None:
+    """The torch module of the operators (g++, a few headers of torch; needs LIB)."""
+    src = os.path.join(CSRC, "fm_ops_torch.cpp")
+    deps = [src, os.path.join(ROOT, "include", "fm_ops.h"), os.path.join(ROOT, "include", "fm_expert.h"),
+            os.path.abspath(__file__)]
+    if not force and os.path.exists(OPS) and all(os.path.getmtime(p) <= os.path.getmtime(OPS) for p in deps):
+        return
+    import torch
+    t = os.path.dirname(os.path.abspath(torch.__file__))
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(t, "include"), "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include"),
+           "-o", OPS + ".tmp", src, "-L", PKG, "-l:libfm_expert.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(t, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(OPS + ".tmp", OPS)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    _build_lib(force, verbose)
+    _build_ops(force)
+    return LIB
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
     if not force and not _stale():
         return LIB
     cmd = [nvcc_path(), "-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC",
