@@ -35,6 +35,7 @@ struct GemmParams {
   void* out;
   int64_t ldsa, ldsw, ldo;
   int m, n, groups, f32;
+  int vec;                 // rows of `out` start on 16-byte boundaries
 };
 
 // 2-D tiled load of a box of 128-byte rows at (column c0, row c1).
@@ -69,225 +70,309 @@ __device__ __forceinline__ void fma2(float& c0, float& c1, float a0, float a1, f
       : "+f"(c0), "+f"(c1)
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// One MMA of a group (kind::f8f6f4, K = 32), ACC 0: a fresh accumulator.
+template <int ACC>
+__device__ __forceinline__ void mma_e4m3_one(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "n"(ACC)
+      : "memory");
+}
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
-__device__ __forceinline__ void store_out(const GemmParams& p, int i, int j, float v) {
+__device__ __forceinline__ float bias_at(const GemmParams& p, int j) {
+  return p.bias != nullptr && j < p.n ? __uint_as_float((uint32_t)p.bias[j] << 16) : 0.f;
+}
+__device__ __forceinline__ void store_out1(const GemmParams& p, int i, int j, float v) {
+  if (j >= p.n) return;
   if (p.f32)
     static_cast<float*>(p.out)[(int64_t)i * p.ldo + j] = v;
   else
     static_cast<__nv_bfloat16*>(p.out)[(int64_t)i * p.ldo + j] = __float2bfloat16_rn(v);
 }
+// Channels j .. j + 7 (j a multiple of 8) of row i where p.vec holds, plus the
+// bias, rounded once to the output type.
+__device__ __forceinline__ void store_out8(const GemmParams& p, int i, int j, const float* v) {
+  if (j + 8 > p.n) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) store_out1(p, i, j + e, v[e] + bias_at(p, j + e));
+    return;
+  }
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = v[e] + bias_at(p, j + e);
+  const int64_t at = (int64_t)i * p.ldo + j;
+  if (p.f32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+    o[0] = make_float4(x[0], x[1], x[2], x[3]);
+    o[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) =
+        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  }
+}
+
+// 4 consecutive scales from group g on (0 past the last); `v4`: 16-byte loads allowed.
+__device__ __forceinline__ float4 scales4(const float* s, int g, int groups, bool v4) {
+  if (v4 && g + 4 <= groups) return *reinterpret_cast<const float4*>(s + g);
+  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (g < groups) r.x = s[g];
+  if (g + 1 < groups) r.y = s[g + 1];
+  if (g + 2 < groups) r.z = s[g + 2];
+  if (g + 3 < groups) r.w = s[g + 3];
+  return r;
+}
 
 // ----------------------------------------------------------------- few rows
-// The weights are the 128-row operand and BT rows of `a` the narrow one, so a
-// single row costs the tensor cores 16 columns and not 128; thread = output
-// channel, so a warp stores 32 consecutive channels of a row.  The blocks of
-// a cluster split the groups of k (there are too few tiles to fill the GPU
-// and the time is that of streaming the weights), leave their sums in shared
-// memory and each adds a share of the rows over all of them in rank order.
-constexpr int kAhead = 8;      // groups of scales brought to shared memory at a time
-
+// A block owns up to 128 rows of `a` (BT of them brought: 16, 32, 64 or 128)
+// x 128 output channels, and the blocks of a cluster split the groups of k:
+// there are too few tiles to fill the GPU, and the time is that of streaming
+// the weights.  The rows are the 128-row operand even when there is one of them:
+// the rows behind BT are whatever shared memory holds and give accumulator rows
+// nobody reads, and a thread is a row, so a group's factor is one register.
+// (With the channels as the 128-row operand the factors differ by column and
+// come from shared memory, whose bandwidth M = 128, N <= 128 products use up:
+// 830 cycles a group against 370 at 50 rows.)  Each block of the cluster leaves
+// its sums in shared memory and adds its share of the tile over all of them in
+// rank order.
 template <int BT>
-struct Narrow {
+struct Few {
   static constexpr int kW = 128 * 128, kStage = kW + BT * 128;
-  static constexpr int kStages = BT == 128 ? 6 : BT == 64 ? 4 : 5;
-  static constexpr int kThreads = 192;
-  static constexpr int kScales = 2 * kAhead * BT * 4;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kScales + 256;
-  static_assert((size_t)kStages * kStage >= (size_t)BT * 128 * 4, "the sums reuse the ring");
+  static constexpr int kStages = BT == 128 ? 6 : 8;
+  static constexpr int kTail = (128 - BT) * 128;       // the last stage's rows behind BT
+  static constexpr int kBufs = 4;                      // accumulators of 128 columns
+  static constexpr int kThreads = 320;                 // TMA, MMA, 8 epilogue warps
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kTail + 256;
+  static_assert(kSmem <= 232448, "227 KB");
+  static_assert((size_t)kStages * kStage >= (size_t)BT * 512, "the sums reuse the ring");
 };
 
 template <int BT>
-__global__ void __launch_bounds__(192, 1)
-narrow_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw,
-              const __grid_constant__ GemmParams p, int split) {
-  using C = Narrow<BT>;
+__global__ void __launch_bounds__(320, 1)
+few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw,
+           const __grid_constant__ GemmParams p, int split) {
+  using C = Few<BT>;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = align1024(raw);
-  float* scales = reinterpret_cast<float*>(ring + (size_t)C::kStages * C::kStage);   // [2][kAhead][BT]
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(scales) + C::kScales);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)C::kStages * C::kStage + C::kTail);
   uint64_t* empty = full + C::kStages;
-  uint64_t* tfull = empty + C::kStages;  // [2]
-  uint64_t* tempty = tfull + 2;          // [2]
-  uint64_t* drain = tempty + 2;
+  uint64_t* tfull = empty + C::kStages;  // [kBufs]
+  uint64_t* tempty = tfull + C::kBufs;   // [kBufs]
+  uint64_t* drain = tempty + C::kBufs;
   uint32_t* slot = reinterpret_cast<uint32_t*>(drain + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const unsigned rank = split > 1 ? cluster_rank() : 0, tile = blockIdx.x / (unsigned)split;
+  const unsigned rt = (unsigned)((p.m + BT - 1) / BT);
+  const int i0 = (int)(tile % rt) * BT, nb = (int)(tile / rt), n0 = nb * 128;
+  const int rows = p.m - i0 < BT ? p.m - i0 : BT;
+  const int quarters = (rows + 31) / 32;               // TMEM lane quarters with rows of `a`
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(smem_u32(&tfull[b]), 1);
-      mbar_init(smem_u32(&tempty[b]), 4);
+      mbar_init(smem_u32(&tempty[b]), 2 * quarters);
     }
     mbar_init(smem_u32(drain), 1);
     fence_mbar_init();
   }
-  constexpr int kCols = 2 * BT;          // a power of two, at least 32
   if (warp == 1) {
-    tmem_alloc(smem_u32(slot), kCols);
+    tmem_alloc(smem_u32(slot), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const unsigned rank = split > 1 ? cluster_rank() : 0, tile = blockIdx.x / (unsigned)split;
-  const unsigned rt = (unsigned)((p.m + BT - 1) / BT);
-  const int i0 = (int)(tile % rt) * BT, nb = (int)(tile / rt), n0 = nb * 128;
   const int g0 = (int)((int64_t)p.groups * rank / split), g1 = (int)((int64_t)p.groups * (rank + 1) / split);
   const int count = g1 - g0;
 
+  // In the TMA and MMA warps all lanes run the loop and one elected lane issues,
+  // so that addresses and descriptors live in uniform registers.
   if (warp == 0) {
-    if (lane == 0) {
-      int it = 0;
-      for (; it < count; ++it) {
-        const int s = it % C::kStages;
-        if (it >= C::kStages && !mbar_wait(smem_u32(&empty[s]), ((it / C::kStages) & 1) ^ 1, kSpin)) {
-          atomicOr(&g_ops_err, 1u);
-          break;
-        }
-        const uint32_t dst = smem_u32(ring + (size_t)s * C::kStage), bar = smem_u32(&full[s]);
-        mbar_arrive_expect_tx(bar, C::kStage);
-        tma_load_2d(dst, &mw, (g0 + it) * 128, n0, bar);
-        tma_load_2d(dst + C::kW, &ma, (g0 + it) * 128, i0, bar);
+    const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), ring0 = smem_u32(ring);
+    uint32_t s = 0, ph = 1;                  // a fresh barrier's previous phase counts as done
+    int it = 0;
+    for (; it < count; ++it) {
+      if (!__all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ph, kSpin))) {
+        if (lane == 0) atomicOr(&g_ops_err, 1u);
+        break;
       }
-      // every issued copy lands before its memory is used for anything else
-      for (int j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
-        mbar_wait(smem_u32(&full[j % C::kStages]), (j / C::kStages) & 1, kSpin);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full0 + 8 * s, C::kStage);
+        tma_load_2d(ring0 + s * C::kStage, &mw, (g0 + it) * 128, n0, full0 + 8 * s);
+        tma_load_2d(ring0 + s * C::kStage + C::kW, &ma, (g0 + it) * 128, i0, full0 + 8 * s);
+      }
+      __syncwarp();
+      if (++s == C::kStages) s = 0, ph ^= 1;
     }
+    // every issued copy lands before its memory is used for anything else
+    for (int j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
+      mbar_wait(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1, kSpin);
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(128, BT);
-      for (int it = 0; it < count; ++it) {
-        const int s = it % C::kStages, b = it & 1;
-        if ((it >= 2 && !mbar_wait(smem_u32(&tempty[b]), ((it >> 1) - 1) & 1, kSpin)) ||
-            !mbar_wait(smem_u32(&full[s]), (it / C::kStages) & 1, kSpin)) {
-          atomicOr(&g_ops_err, 2u);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t w = smem_u32(ring + (size_t)s * C::kStage);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_e4m3(tmem + b * BT, desc_sw128(w + j * 32), desc_sw128(w + C::kW + j * 32), idesc, j != 0);
-        mma_commit(smem_u32(&empty[s]));
-        mma_commit(smem_u32(&tfull[b]));
-      }
-      mma_commit(smem_u32(drain));             // every MMA is done before TMEM and the ring are given up
-      mbar_wait(smem_u32(drain), 0, kSpin);
-    }
-  } else {
-    const int et = threadIdx.x - 64;           // 0 .. 127
-    const int row = 32 * (warp & 3) + lane;    // TMEM lane: output channel n0 + row
-    const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const float* sw = p.sw + (int64_t)nb * p.ldsw + g0;
-    // Scales of kAhead groups: this thread brings row i0 + st, groups sg, sg + kPer, ...
-    constexpr int kPer = 128 / BT;
-    constexpr int kMine = kAhead / kPer > 0 ? kAhead / kPer : 1;
-    const int st = et % BT, sg = et / BT;
-    const bool srow = i0 + st < p.m && sg < kAhead;
-    const float* sa = p.sa + (int64_t)(i0 + st) * p.ldsa + g0;
-    float next[kMine];
-    auto fetch = [&](int base) {
-#pragma unroll
-      for (int q = 0; q < kMine; ++q) {
-        const int g = base + sg + q * kPer;
-        next[q] = srow && g < count ? sa[g] * sw[g] : 0.f;
-      }
-    };
-    auto keep = [&](int buf) {
-#pragma unroll
-      for (int q = 0; q < kMine; ++q)
-        if (sg + q * kPer < kAhead) scales[(buf * kAhead + sg + q * kPer) * BT + st] = next[q];
-    };
-    float acc[BT];
-#pragma unroll
-    for (int c = 0; c < BT; ++c) acc[c] = 0.f;
-    bool ok = true;
-    fetch(0);
+    constexpr uint32_t idesc = idesc_e4m3(128, 128);
+    const uint64_t d0 = desc_sw128(smem_u32(ring));
+    const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), tfull0 = smem_u32(tfull), tempty0 = smem_u32(tempty);
+    uint32_t s = 0, ph = 0, b = 0, bph = 1;
     for (int it = 0; it < count; ++it) {
-      const int b = it & 1, sb = (it / kAhead) & 1;
-      if (it % kAhead == 0) {
-        keep(sb);
-        named_bar_sync(1, 128);
-        fetch(it + kAhead);
-      }
-      if (!ok) continue;                       // after a timeout: only the barrier, which the warps share
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tfull[b]), (it >> 1) & 1, kSpin));
-      if (!ok) {
-        if (lane == 0) atomicOr(&g_ops_err, 4u);
-        continue;
+      if (!__all_sync(0xffffffffu, mbar_wait(tempty0 + 8 * b, bph, kSpin) && mbar_wait(full0 + 8 * s, ph, kSpin))) {
+        if (lane == 0) atomicOr(&g_ops_err, 2u);
+        break;
       }
       tc_fence_after();
-      const float* s = scales + (sb * kAhead + it % kAhead) * BT;
-      if constexpr (BT == 16) {
-        float v[16];
-        tmem_ld16(ta + b * BT, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(s + e);
-          fma2(acc[e], acc[e + 1], v[e], v[e + 1], f.x, f.y);
-          fma2(acc[e + 2], acc[e + 3], v[e + 2], v[e + 3], f.z, f.w);
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < BT / 32; ++q) {
-          float v[32];
-          tmem_ld32(ta + b * BT + q * 32, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(s + q * 32 + e);
-            float* a = acc + q * 32 + e;
-            fma2(a[0], a[1], v[e], v[e + 1], f.x, f.y);
-            fma2(a[2], a[3], v[e + 2], v[e + 3], f.z, f.w);
-          }
-        }
+      if (elect_one()) {
+        const uint64_t wd = d0 + s * (C::kStage >> 4), ad = wd + (C::kW >> 4);
+        mma_e4m3_one<0>(tmem + b * 128, ad, wd, idesc);
+        mma_e4m3_one<1>(tmem + b * 128, ad + 2, wd + 2, idesc);
+        mma_e4m3_one<1>(tmem + b * 128, ad + 4, wd + 4, idesc);
+        mma_e4m3_one<1>(tmem + b * 128, ad + 6, wd + 6, idesc);
+        mma_commit(tfull0 + 8 * b);
+        mma_commit(empty0 + 8 * s);
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&tempty[b]));
+      if (++s == C::kStages) s = 0, ph ^= 1;
+      if (++b == C::kBufs) b = 0, bph ^= 1;
     }
-    const int rows = p.m - i0 < BT ? p.m - i0 : BT;
-    if (split == 1) {
-      const int j = n0 + row;
-      if (ok && j < p.n) {
-        const float bias = p.bias != nullptr ? __uint_as_float((uint32_t)p.bias[j] << 16) : 0.f;
+    if (elect_one()) mma_commit(smem_u32(drain));   // every MMA is done before TMEM and the ring are given up
+    __syncwarp();
+    mbar_wait(smem_u32(drain), 0, kSpin);
+  } else if ((warp & 3) < quarters) {
+    const int q4 = warp & 3, h = (warp - 2) >> 2;
+    const int row = 32 * q4 + lane;            // TMEM lane: row i0 + row
+    const bool live = row < rows;
+    const uint32_t ta = tmem + ((uint32_t)(32 * q4) << 16) + h * 64;
+    const float* sa = p.sa + (int64_t)(i0 + (live ? row : 0)) * p.ldsa + g0;
+    const float* sw = p.sw + (int64_t)nb * p.ldsw + g0;
+    const bool v4 = (reinterpret_cast<uintptr_t>(sa) & 15) == 0;
+    float acc[64];
 #pragma unroll
-        for (int c = 0; c < BT; ++c)
-          if (c < rows) store_out(p, i0 + c, j, acc[c] + bias);
+    for (int c = 0; c < 64; ++c) acc[c] = 0.f;
+    bool ok = true;
+    // scales of four groups of this row in hand and four on the way
+    float4 fa = scales4(sa, 0, count, v4), fn = scales4(sa, 4, count, v4);
+    float wn = sw[0];
+    uint32_t b = 0, bph = 0;
+    for (int it = 0; it < count; ++it) {
+      const float s = fa.x * wn;
+      if (it + 1 < count) wn = sw[it + 1];
+      if ((it & 3) == 3) {
+        fa = fn;
+        fn = scales4(sa, it + 5, count, v4);
+      } else {
+        fa.x = fa.y;
+        fa.y = fa.z;
+        fa.z = fa.w;
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tfull[b]), bph, kSpin));
+      if (!ok) {
+        if (lane == 0) atomicOr(&g_ops_err, 4u);
+        break;
+      }
+      tc_fence_after();
+      float v[2][16];
+      tmem_ld16(ta + b * 128, v[0]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        tmem_ld_wait();
+        if (q < 3) {
+          tmem_ld16(ta + b * 128 + (q + 1) * 16, v[(q + 1) & 1]);
+        } else {                               // all read: the accumulator goes back
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&tempty[b]));
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 2)
+          fma2(acc[q * 16 + e], acc[q * 16 + e + 1], v[q & 1][e], v[q & 1][e + 1], s, s);
+      }
+      if (++b == C::kBufs) b = 0, bph ^= 1;
+    }
+    if (split == 1 && p.vec) {
+      if (ok && live) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 8) store_out8(p, i0 + row, n0 + h * 64 + c, acc + c);
       }
     } else {
-      // the ring is free: every MMA that reads it has completed (the last tfull)
-      float* part = reinterpret_cast<float*>(ring);          // [BT][128]
+      // the ring is free: every MMA that reads it has completed (the last tfull).
+      // [row][128], 16-byte pieces swizzled by the row
+      float* part = reinterpret_cast<float*>(ring) + row * 128;
+      if (live) {
 #pragma unroll
-      for (int c = 0; c < BT; ++c)
-        if (c < rows) part[c * 128 + row] = acc[c];
+        for (int c = 0; c < 16; ++c)
+          *reinterpret_cast<float4*>(part + (((h * 16 + c) ^ (row & 31)) << 2)) =
+              make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+      }
     }
   }
   __syncwarp();
-  if (split > 1) {
+  if (split > 1 || !p.vec) {
     cluster_sync_all();
     if (warp >= 2) {
-      const int rows = p.m - i0 < BT ? p.m - i0 : BT;
-      const int c0 = rows * (int)rank / split, c1 = rows * ((int)rank + 1) / split;
-      const int row = threadIdx.x - 64, j = n0 + row;
-      const float bias = j < p.n && p.bias != nullptr ? __uint_as_float((uint32_t)p.bias[j] << 16) : 0.f;
-      for (int c = c0; c < c1; ++c) {
-        const uint32_t at = smem_u32(reinterpret_cast<float*>(ring) + c * 128 + row);
-        float v[8];
+      const float* part = reinterpret_cast<const float*>(ring);
+      if (p.vec) {
+        // this rank's share of the tile's rows x 16 pieces of 8 channels
+        const int all = rows * 16, c0 = all * (int)rank / split, c1 = all * ((int)rank + 1) / split;
+        for (int c = c0 + (int)threadIdx.x - 64; c < c1; c += C::kThreads - 64) {
+          const int r = c >> 4, piece = c & 15;
+          const uint32_t at = smem_u32(part + r * 128);
+          const uint32_t lo = at + (((2 * piece) ^ (r & 31)) << 4), hi = at + (((2 * piece + 1) ^ (r & 31)) << 4);
+          float sum[8] = {};
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < split) v[r] = ld_dsmem_f1(map_shared_rank(at, r));
-        float sum = v[0];
+          for (int k = 0; k < 8; ++k) {
+            if (k < split) {
+              const float4 x = ld_dsmem_f4(map_shared_rank(lo, k)), y = ld_dsmem_f4(map_shared_rank(hi, k));
+              sum[0] += x.x;
+              sum[1] += x.y;
+              sum[2] += x.z;
+              sum[3] += x.w;
+              sum[4] += y.x;
+              sum[5] += y.y;
+              sum[6] += y.z;
+              sum[7] += y.w;
+            }
+          }
+          store_out8(p, i0 + r, n0 + piece * 8, sum);
+        }
+      } else {
+        // rows at any element: a warp takes four rows of this rank's share at a
+        // time and stores 32 neighbours of one with each instruction
+        const int c0 = rows * (int)rank / split, c1 = rows * ((int)rank + 1) / split;
+        float bias[4];
 #pragma unroll
-        for (int r = 1; r < 8; ++r)
-          if (r < split) sum += v[r];
-        if (j < p.n) store_out(p, i0 + c, j, sum + bias);
+        for (int q = 0; q < 4; ++q) bias[q] = bias_at(p, n0 + 32 * q + lane);
+        for (int r = c0 + 4 * (warp - 2); r < c1; r += 32) {
+          float sum[4][4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum[u][q] = 0.f;
+          for (int k = 0; k < split; ++k) {
+            const uint32_t base = map_shared_rank(smem_u32(part), k);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (r + u < c1)
+                  sum[u][q] += ld_dsmem_f1(base + (r + u) * 512 + (((8 * q + (lane >> 2)) ^ ((r + u) & 31)) << 4) +
+                                           ((lane & 3) << 2));
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (r + u < c1) store_out1(p, i0 + r + u, n0 + 32 * q + lane, sum[u][q] + bias[q]);
+        }
       }
     }
     cluster_sync_all();                        // no block leaves while another reads its sums
@@ -296,14 +381,14 @@ narrow_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CU
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kCols);
+    tmem_dealloc(tmem, 512);
   }
 }
 
 template <int BT>
-cudaError_t launch_narrow(const CUtensorMap& ma, const CUtensorMap& mw, const GemmParams& p, int split, cudaStream_t st) {
-  using C = Narrow<BT>;
-  cudaError_t e = cudaFuncSetAttribute(narrow_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+cudaError_t launch_few(const CUtensorMap& ma, const CUtensorMap& mw, const GemmParams& p, int split, cudaStream_t st) {
+  using C = Few<BT>;
+  cudaError_t e = cudaFuncSetAttribute(few_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (((int64_t)p.m + BT - 1) / BT) * (((int64_t)p.n + 127) / 128);
   cudaLaunchConfig_t cfg = {};
@@ -316,8 +401,8 @@ cudaError_t launch_narrow(const CUtensorMap& ma, const CUtensorMap& mw, const Ge
   at[0].val.clusterDim.x = (unsigned)split;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, narrow_kernel<BT>, ma, mw, p, split);
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, few_kernel<BT>, ma, mw, p, split);
 }
 
 // ----------------------------------------------------------------- many rows
@@ -367,12 +452,6 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d, uint64_t ad, uint64_t 
       "l"(ad), "l"(bd), "r"(idesc), "n"(ACC)
       : "memory");
 }
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
 // Arrives on `bar` of both blocks of the pair when this thread's MMAs are done.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
   asm volatile(
@@ -396,17 +475,6 @@ __device__ __forceinline__ TileAt tile_at(unsigned t, unsigned mts, unsigned nts
   const unsigned band = t / (8 * nts), r = t - band * 8 * nts;
   const unsigned h = mts - band * 8 < 8 ? mts - band * 8 : 8;
   return TileAt{(int)(band * 8 + r % h), (int)(r / h)};
-}
-
-// 4 consecutive scales from group g on (0 past the last); `v4`: 16-byte loads allowed.
-__device__ __forceinline__ float4 scales4(const float* s, int g, int groups, bool v4) {
-  if (v4 && g + 4 <= groups) return *reinterpret_cast<const float4*>(s + g);
-  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (g < groups) r.x = s[g];
-  if (g + 1 < groups) r.y = s[g + 1];
-  if (g + 2 < groups) r.z = s[g + 2];
-  if (g + 3 < groups) r.w = s[g + 3];
-  return r;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
@@ -711,6 +779,34 @@ cudaError_t launch_wide(const CUtensorMap& ma, const CUtensorMap& mw, const CUte
   return cudaGetLastError();
 }
 
+// Which kernel, how many rows a block brings and how often k is split: the
+// smallest estimated time.  The figures (microseconds) were fitted to sweeps of
+// both kernels over 1 .. 16384 rows, 512 .. 8192 channels and 2 .. 128 groups:
+// a block of few_kernel takes 0.24 a group whatever it holds (one CTA issuing
+// four products and their commits), a pair of wide_kernel 0.45 for four times
+// as much, and adding the sums of a split costs by rows and blocks.
+struct Choice {
+  bool wide;
+  int bt, split;
+};
+Choice choose(int64_t m, int64_t n, int64_t groups, int sms) {
+  Choice best{false, m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128, 1};
+  const int64_t tiles = (m + best.bt - 1) / best.bt * ((n + 127) / 128);
+  const double rows = m < best.bt ? (double)m : best.bt;
+  double least = 1e30;
+  for (int s = 1; s <= 8 && s <= groups; s *= 2) {
+    // clusters need their blocks on neighbouring SMs: 120 of 148 SMs take clusters of 8
+    const int64_t room = s <= 2 ? sms : s == 4 ? sms * 136 / 148 : sms * 120 / 148;
+    const int64_t waves = (tiles * s + room - 1) / room;
+    const double t = 2.3 + waves * (waves > 1 ? 2.8 + 0.28 * ((groups + s - 1) / s) : 2.0 + 0.24 * ((groups + s - 1) / s)) +
+                     (s > 1 ? 0.1 + rows * (0.014 + 0.003 * s) : 0.0);
+    if (t < least) least = t, best.split = s;
+  }
+  const int64_t pairs = sms / 2, waves = (((m + 255) / 256) * ((n + 255) / 256) + pairs - 1) / pairs;
+  if (6.0 + waves * (1.1 + 0.45 * groups) < least) best.wide = true;
+  return best;
+}
+
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -790,16 +886,13 @@ fm_status fm_gemm_e4m3_b128(const uint8_t* a, int64_t lda, const float* sa, int6
   if (bias != nullptr) FM_TRY(c.rows(bias, "bias", n, n, 1, 2, 2));
   FM_TRY(c.rows(out, "out", ldo, n, m, out_type == FM_F32 ? 4 : 2, out_type == FM_F32 ? 4 : 2));
   FM_TRY(c.memory());
-  const int sms = fm::sm_count(c.device);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const fm::GemmParams p{sa, sw, bias, out, ldsa, ldsw, ldo, m, n, (int)groups, out_type == FM_F32};
-  const bool wide = m > 256 && (int64_t)m * n >= 256 * 256 * 24;
-  int bt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
-  int split = 1;
-  if (!wide) {
-    const int64_t few = (((int64_t)m + bt - 1) / bt) * (((int64_t)n + 127) / 128);
-    while (split < 8 && split * 2 <= groups && few * split * 2 <= sms * (bt <= 64 ? 2 : 1)) split *= 2;
-  }
+  const size_t es = out_type == FM_F32 ? 4 : 2;
+  const bool vec = ((uintptr_t)out & 15) == 0 && (m <= 1 || ((uint64_t)ldo * es) % 16 == 0);
+  const fm::GemmParams p{sa, sw, bias, out, ldsa, ldsw, ldo, m, n, (int)groups, out_type == FM_F32, vec};
+  const fm::Choice pick = fm::choose(m, n, (int)groups, fm::sm_count(c.device));
+  const bool wide = pick.wide;
+  const int bt = pick.bt, split = pick.split;
   CUtensorMap ma, mw, mo;
   if (!fm::codes_map(&ma, a, lda, m, k, wide ? 128 : bt) || !fm::codes_map(&mw, w, ldw, n, k, wide ? 64 : 128))
     return c.fail(FM_ERR_CUDA, "the tensor maps of a and w were refused (m %d, n %d, k %d, strides %lld, %lld)", m, n, k,
@@ -809,10 +902,10 @@ fm_status fm_gemm_e4m3_b128(const uint8_t* a, int64_t lda, const float* sa, int6
     if (!tma_out) mo = ma;
     return c.launched(fm::launch_wide(ma, mw, mo, p, tma_out, c.device, st));
   }
-  return c.launched(bt == 16   ? fm::launch_narrow<16>(ma, mw, p, split, st)
-                    : bt == 32 ? fm::launch_narrow<32>(ma, mw, p, split, st)
-                    : bt == 64 ? fm::launch_narrow<64>(ma, mw, p, split, st)
-                               : fm::launch_narrow<128>(ma, mw, p, split, st));
+  return c.launched(bt == 16   ? fm::launch_few<16>(ma, mw, p, split, st)
+                    : bt == 32 ? fm::launch_few<32>(ma, mw, p, split, st)
+                    : bt == 64 ? fm::launch_few<64>(ma, mw, p, split, st)
+                               : fm::launch_few<128>(ma, mw, p, split, st));
 }
 
 fm_status fm_ops_sync(void* stream) {
