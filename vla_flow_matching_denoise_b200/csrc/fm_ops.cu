@@ -104,6 +104,8 @@ struct NormParams {
 template <typename TX, typename TH, int NP>
 __global__ void norm_kernel(const NormParams p) {
   __shared__ float part[32];
+  grid_dep_launch();
+  grid_dep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int slot = warp / p.wpr;                              // row of this block
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / (32 * p.wpr)) + slot;
@@ -186,13 +188,9 @@ cudaError_t launch_norm(NormParams p, cudaStream_t st) {
   const int rpb = p.wpr >= 8 ? 1 : 8 / p.wpr;
   const unsigned grid = (unsigned)(((int64_t)p.rows + rpb - 1) / rpb);
   const int threads = rpb * p.wpr * 32;
-  if (np == 1)
-    norm_kernel<TX, TH, 1><<<grid, threads, 0, st>>>(p);
-  else if (np == 2)
-    norm_kernel<TX, TH, 2><<<grid, threads, 0, st>>>(p);
-  else
-    norm_kernel<TX, TH, 4><<<grid, threads, 0, st>>>(p);
-  return cudaGetLastError();
+  return np == 1   ? launch_op(norm_kernel<TX, TH, 1>, grid, threads, 0, 1, st, p)
+         : np == 2 ? launch_op(norm_kernel<TX, TH, 2>, grid, threads, 0, 1, st, p)
+                   : launch_op(norm_kernel<TX, TH, 4>, grid, threads, 0, 1, st, p);
 }
 
 // ----------------------------------------------------------------- gated activation
@@ -207,16 +205,32 @@ struct GatedParams {
   int rpb;                 //   so many whole rows per block
 };
 
+// act(g) u with both activations as g / (1 + exp(-t)): SiLU has t = g, and
+// (1 + tanh(z)) / 2 = 1 / (1 + exp(-2 z)) makes the tanh form of GELU one with
+// t = 2 z, without its cancellation for negative z.  Two approximate
+// instructions (2^x and 1/x, about 2^-22 each) and six more: with expf and a
+// true division the kernel was bound by instructions (96 us at 16384 x 4096,
+// memory 52).  An overflow of the exponential gives 1/inf = 0, the limit.
 template <int ACT>
 __device__ __forceinline__ float gated(float g, float u) {
-  if (ACT == FM_ACT_SILU) return g / (1.0f + __expf(-g)) * u;
-  // 1 + tanh(z) = 2 / (1 + exp(-2 z)): no cancellation for negative z
-  const float z = 0.7978845608028654f * fmaf(0.044715f * g * g, g, g);
-  return g / (1.0f + __expf(-2.0f * z)) * u;
+  constexpr float kLog2e = 1.4426950408889634f;
+  float t;   // -t log2(e)
+  if (ACT == FM_ACT_SILU) {
+    t = -kLog2e * g;
+  } else {
+    constexpr float c = -2.0f * 0.7978845608028654f * kLog2e;
+    t = g * fmaf(c * 0.044715f, g * g, c);
+  }
+  float e, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r * u;
 }
 
 template <typename T, int ACT>
 __global__ void __launch_bounds__(256) gated_kernel(const GatedParams p) {
+  grid_dep_launch();
+  grid_dep_wait();
   const int lane = threadIdx.x & 31;
   int64_t row;
   int c;
@@ -267,13 +281,9 @@ cudaError_t launch_gated(GatedParams p, fm_act act, cudaStream_t st) {
     grid = ((int64_t)p.rows + p.rpb - 1) / p.rpb;
   }
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  if (act == FM_ACT_SILU)
-    gated_kernel<T, FM_ACT_SILU><<<(unsigned)grid, threads, 0, st>>>(p);
-  else if (act == FM_ACT_GELU_TANH)
-    gated_kernel<T, FM_ACT_GELU_TANH><<<(unsigned)grid, threads, 0, st>>>(p);
-  else
-    gated_kernel<T, FM_ACT_NONE><<<(unsigned)grid, threads, 0, st>>>(p);
-  return cudaGetLastError();
+  return act == FM_ACT_SILU        ? launch_op(gated_kernel<T, FM_ACT_SILU>, (unsigned)grid, threads, 0, 1, st, p)
+         : act == FM_ACT_GELU_TANH ? launch_op(gated_kernel<T, FM_ACT_GELU_TANH>, (unsigned)grid, threads, 0, 1, st, p)
+                                   : launch_op(gated_kernel<T, FM_ACT_NONE>, (unsigned)grid, threads, 0, 1, st, p);
 }
 
 // ----------------------------------------------------------------- weight quantiser
@@ -283,6 +293,8 @@ __global__ void __launch_bounds__(256) quantize_weight_kernel(const uint16_t* __
                                                               uint8_t* __restrict__ codes, int64_t ldc,
                                                               float* __restrict__ scales, int64_t lds) {
   __shared__ float part[8];
+  grid_dep_launch();
+  grid_dep_wait();
   const unsigned gk = (unsigned)((k + 127) / 128);
   const int64_t n0 = (int64_t)(blockIdx.x / gk) * 128;
   const int k0 = (int)(blockIdx.x % gk) * 128;
@@ -305,16 +317,18 @@ __global__ void __launch_bounds__(256) quantize_weight_kernel(const uint16_t* __
 }
 
 // ----------------------------------------------------------------- multi-axis RoPE
-// The cosines and sines of a tile of rows are made once, in shared memory, for
-// all of its heads; the angle is reduced to a fraction of a turn in 64 bits
-// (positions x frequency passes 2^20 turns, where fp32 has no digits left).
+// A thread owns V consecutive pairs of one row and walks over heads with their
+// cosines and sines in registers, so they are made once for all heads of its
+// share; few rows split the heads over more threads instead.  The angle is
+// reduced to a fraction of a turn in 64 bits (positions x frequency pass 2^20
+// turns, where fp32 has no digits left).
 constexpr int kMaxPairs = 128;
 struct RopeParams {
   const void* x;
   const int32_t* pos;
   void *q, *k, *v;
   int64_t ldx, ldp, ldq, ldk, ldv;
-  int rows, nq, nkv, hd, n, tt;       // tt: rows per tile
+  int rows, nq, nkv, hd, n, parts;    // parts: shares of the heads
   double turn[kMaxPairs];             // frequency in turns per position
   uint8_t axis[kMaxPairs];
 };
@@ -339,92 +353,87 @@ __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
     for (int i = 0; i < V; ++i) from_f(p + i, v[i]);
   }
 }
+// V elements as they are.
+template <typename T, int V>
+__device__ __forceinline__ void copy_v(const T* src, T* dst) {
+  if constexpr (V == 8) {
+#pragma unroll
+    for (int i = 0; i < (int)(8 * sizeof(T) / 16); ++i) reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) dst[i] = src[i];
+  }
+}
 
 template <typename T, int V>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ float2 cs[];      // [tt][n]
   __shared__ double turn[kMaxPairs];
   __shared__ uint8_t axis[kMaxPairs];
-  const int tid = threadIdx.x, n = p.n;
-  for (int j = tid; j < n; j += blockDim.x) {
+  grid_dep_launch();
+  for (int j = threadIdx.x; j < p.n; j += blockDim.x) {
     turn[j] = p.turn[j];
     axis[j] = p.axis[j];
   }
-  const int heads = p.nq + p.nkv;
-  const int rot = n / V, tail = (p.hd - 2 * n) / V, val = p.v != nullptr ? p.nkv * (p.hd / V) : 0;
-  const int u_rot = heads * rot, u_tail = heads * tail, units = u_rot + u_tail + val;
-  for (int64_t r0 = (int64_t)blockIdx.x * p.tt; r0 < p.rows; r0 += (int64_t)gridDim.x * p.tt) {
-    const int tt = (int)(p.rows - r0 < p.tt ? p.rows - r0 : p.tt);
-    __syncthreads();                  // the tables above; the previous tile's cs
-    for (int i = tid; i < tt * n; i += blockDim.x) {
-      const int t = i / n, j = i - t * n;
-      const double a = (double)p.pos[(int64_t)axis[j] * p.ldp + r0 + t] * turn[j];
-      float s, c;
-      sincospif(2.0f * (float)(a - rint(a)), &s, &c);
-      cs[i] = make_float2(c, s);
-    }
-    __syncthreads();
-    for (int i = tid; i < tt * units; i += blockDim.x) {
-      const int t = i / units;
-      int u = i - t * units;
-      const int64_t row = r0 + t;
-      const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-      if (u < u_rot) {
-        const int head = u / rot, j = (u - head * rot) * V;
-        T* out = head < p.nq ? static_cast<T*>(p.q) : static_cast<T*>(p.k);
-        if (out == nullptr) continue;
-        out += head < p.nq ? row * p.ldq + head * p.hd : row * p.ldk + (head - p.nq) * p.hd;
-        float lo[V], hi[V], a[V], b[V];
-        load_v<T, V>(x + head * p.hd + j, lo);
-        load_v<T, V>(x + head * p.hd + j + n, hi);
+  __syncthreads();
+  grid_dep_wait();
+  const int per = p.n / V;                                    // threads per row and share
+  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t slot = id / per;
+  const int j = (int)(id - slot * per) * V;
+  const int64_t row = slot / p.parts;
+  const int part = (int)(slot - row * p.parts);
+  if (row >= p.rows) return;
+  float c[V], s[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float2 w = cs[t * n + j + e];
-          a[e] = lo[e] * w.x - hi[e] * w.y;
-          b[e] = hi[e] * w.x + lo[e] * w.y;
-        }
-        store_v<T, V>(out + j, a);
-        store_v<T, V>(out + j + n, b);
-      } else {
-        u -= u_rot;
-        const T* src;
-        T* out;
-        if (u < u_tail) {
-          const int head = u / tail, e = 2 * n + (u - head * tail) * V;
-          out = head < p.nq ? static_cast<T*>(p.q) : static_cast<T*>(p.k);
-          if (out == nullptr) continue;
-          out += (head < p.nq ? row * p.ldq + head * p.hd : row * p.ldk + (head - p.nq) * p.hd) + e;
-          src = x + head * p.hd + e;
-        } else {
-          const int e = (u - u_tail) * V;
-          out = static_cast<T*>(p.v) + row * p.ldv + e;
-          src = x + heads * p.hd + e;
-        }
-        float w[V];
-        load_v<T, V>(src, w);
-        store_v<T, V>(out, w);
-      }
+  for (int e = 0; e < V; ++e) {
+    const double a = (double)p.pos[(int64_t)axis[j + e] * p.ldp + row] * turn[j + e];
+    sincospif(2.0f * (float)(a - rint(a)), &s[e], &c[e]);
+  }
+  const int heads = p.nq + p.nkv, n = p.n, hd = p.hd;
+  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+  T* q = static_cast<T*>(p.q);
+  T* k = static_cast<T*>(p.k);
+  if (q != nullptr) q += row * p.ldq;
+  if (k != nullptr) k += row * p.ldk - (int64_t)p.nq * hd;
+#pragma unroll 4
+  for (int h = part; h < heads; h += p.parts) {
+    T* out = h < p.nq ? q : k;
+    if (out == nullptr) continue;
+    const T* in = x + h * hd;
+    out += h * hd;
+    float lo[V], hi[V], a[V], b[V];
+    load_v<T, V>(in + j, lo);
+    load_v<T, V>(in + j + n, hi);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      // spelled out, so that both widths round alike
+      a[e] = __fmaf_rn(lo[e], c[e], -__fmul_rn(hi[e], s[e]));
+      b[e] = __fmaf_rn(hi[e], c[e], __fmul_rn(lo[e], s[e]));
     }
+    store_v<T, V>(out + j, a);
+    store_v<T, V>(out + j + n, b);
+    for (int e = 2 * n + j; e < hd; e += n) copy_v<T, V>(in + e, out + e);
+  }
+  if (p.v != nullptr) {
+    const T* in = x + heads * hd;
+    T* out = static_cast<T*>(p.v) + row * p.ldv;
+    const int step = p.parts * n;
+    for (int e = part * n + j; e < p.nkv * hd; e += step) copy_v<T, V>(in + e, out + e);
   }
 }
 
 template <typename T>
 cudaError_t launch_rope(RopeParams& p, bool wide, int sms, cudaStream_t st) {
-  const int v = wide ? 8 : 1;
-  const int units = ((p.nq + p.nkv) * (p.hd - p.n) + (p.v ? p.nkv * p.hd : 0)) / v;
-  int tt = 512 / (units > 0 ? units : 1);
-  tt = tt < 1 ? 1 : tt > 16 ? 16 : tt;
-  while (tt > 1 && (int64_t)p.rows < (int64_t)tt * sms * 4) tt >>= 1;   // few rows: spread them
-  p.tt = tt;
-  const int64_t tiles = ((int64_t)p.rows + tt - 1) / tt;
-  const int64_t most = (int64_t)sms * 8;
-  const unsigned grid = (unsigned)(tiles < most ? tiles : most);
-  const size_t smem = (size_t)tt * p.n * sizeof(float2);                // at most 16 KB
-  if (wide)
-    rope_kernel<T, 8><<<grid, 256, smem, st>>>(p);
-  else
-    rope_kernel<T, 1><<<grid, 256, smem, st>>>(p);
-  return cudaGetLastError();
+  const int per = wide ? p.n / 8 : p.n, heads = p.nq + p.nkv;
+  // Shares of the heads: enough threads to fill the GPU (1024 per SM), and no
+  // more than that, because each share makes the row's cosines and sines again.
+  int64_t parts = (int64_t)sms * 1024 / ((int64_t)p.rows * per);
+  parts = parts < 1 ? 1 : parts > heads ? heads : parts;
+  p.parts = parts < 1 ? 1 : (int)parts;
+  const int64_t grid = ((int64_t)p.rows * p.parts * per + 255) / 256;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return wide ? launch_op(rope_kernel<T, 8>, (unsigned)grid, 256, 0, 1, st, p)
+              : launch_op(rope_kernel<T, 1>, (unsigned)grid, 256, 0, 1, st, p);
 }
 
 bool mult16(const void* p, int64_t ld, size_t elem, int rows) {
@@ -574,9 +583,8 @@ fm_status fm_quantize_weight_e4m3_b128(const uint16_t* w, int64_t ldw, int n, in
   FM_TRY(c.rows(codes, "codes", ldc, k, n, 1, 1));
   FM_TRY(c.rows(scales, "scales", lds, gk, (int)gn, 4, 4));
   FM_TRY(c.memory());
-  fm::quantize_weight_kernel<<<(unsigned)(gn * gk), 256, 0, static_cast<cudaStream_t>(stream)>>>(w, ldw, n, k, codes, ldc,
-                                                                                               scales, lds);
-  return c.launched(cudaGetLastError());
+  return c.launched(fm::launch_op(fm::quantize_weight_kernel, (unsigned)(gn * gk), 256, 0, 1,
+                                  static_cast<cudaStream_t>(stream), w, ldw, n, k, codes, ldc, scales, lds));
 }
 
 fm_status fm_rope_axes(const void* x, fm_dtype type, int64_t ldx, int rows, int n_q, int n_kv, int head_dim,
@@ -619,7 +627,7 @@ fm_status fm_rope_axes(const void* x, fm_dtype type, int64_t ldx, int rows, int 
   FM_TRY(c.memory());
   p.x = x; p.pos = positions; p.q = q_out; p.k = k_out; p.v = v_out;
   p.ldx = ldx; p.ldp = ldp; p.ldq = ldq; p.ldk = ldk; p.ldv = ldv;
-  p.rows = rows; p.nq = n_q; p.nkv = n_kv; p.hd = head_dim; p.n = n_pairs; p.tt = 1;
+  p.rows = rows; p.nq = n_q; p.nkv = n_kv; p.hd = head_dim; p.n = n_pairs; p.parts = 1;
   const bool wide = head_dim % 8 == 0 && n_pairs % 8 == 0 && fm::mult16(x, ldx, es, rows) &&
                     fm::mult16(q_out, ldq, es, q_out ? rows : 0) && fm::mult16(k_out, ldk, es, k_out ? rows : 0) &&
                     fm::mult16(v_out, ldv, es, v_out ? rows : 0);

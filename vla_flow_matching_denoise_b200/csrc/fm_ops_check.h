@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <utility>
 
 #include "../../include/fm_ops.h"
 #include "fm_launch.h"
@@ -27,6 +28,29 @@ struct OpCheck {
   // FM_OK, or FM_ERR_CUDA with the error's text (and the error cleared).
   fm_status launched(cudaError_t e);
 };
+
+// Launches with programmatic dependent launch (every kernel of these operators
+// lets its successor start at once and touches memory only after
+// griddepcontrol.wait, so set-up overlaps the predecessor's end), in clusters of
+// `cluster` blocks.
+template <typename... Params, typename... Args>
+cudaError_t launch_op(void (*kernel)(Params...), unsigned grid, int block, size_t smem, int cluster, cudaStream_t st,
+                      Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3((unsigned)block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
 // Multiprocessors of `device`.
 int sm_count(int device);

@@ -195,6 +195,8 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
+  grid_dep_launch();
+  grid_dep_wait();                           // everything above touches this block's memory only
   const int g0 = (int)((int64_t)p.groups * rank / split), g1 = (int)((int64_t)p.groups * (rank + 1) / split);
   const int count = g1 - g0;
 
@@ -391,18 +393,7 @@ cudaError_t launch_few(const CUtensorMap& ma, const CUtensorMap& mw, const GemmP
   cudaError_t e = cudaFuncSetAttribute(few_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (((int64_t)p.m + BT - 1) / BT) * (((int64_t)p.n + 127) / 128);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * split));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, few_kernel<BT>, ma, mw, p, split);
+  return launch_op(few_kernel<BT>, (unsigned)(tiles * split), C::kThreads, C::kSmem, split, st, ma, mw, p, split);
 }
 
 // ----------------------------------------------------------------- many rows
@@ -477,7 +468,7 @@ __device__ __forceinline__ TileAt tile_at(unsigned t, unsigned mts, unsigned nts
   return TileAt{(int)(band * 8 + r % h), (int)(r / h)};
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(384, 1)
 wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw,
             const __grid_constant__ CUtensorMap mo, const __grid_constant__ GemmParams p, int tma_out) {
   using C = Wide;
@@ -515,6 +506,8 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
   cluster_sync_all();                        // both blocks' barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *slot;
+  grid_dep_launch();
+  grid_dep_wait();                           // everything above touches this pair's memory only
   const unsigned mts = (unsigned)((p.m + 255) / 256), nts = (unsigned)((p.n + 255) / 256);
   const unsigned tiles = mts * nts, pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
 
@@ -775,8 +768,7 @@ cudaError_t launch_wide(const CUtensorMap& ma, const CUtensorMap& mw, const CUte
   const int64_t tiles = (((int64_t)p.m + 255) / 256) * (((int64_t)p.n + 255) / 256);
   const int pairs = wide_pairs(device);
   const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
-  wide_kernel<<<grid, Wide::kThreads, Wide::kSmem, st>>>(ma, mw, mo, p, tma_out ? 1 : 0);
-  return cudaGetLastError();
+  return launch_op(wide_kernel, grid, Wide::kThreads, Wide::kSmem, 2, st, ma, mw, mo, p, tma_out ? 1 : 0);
 }
 
 // Which kernel, how many rows a block brings and how often k is split: the
