@@ -120,9 +120,9 @@ fm_status fm_gemm_e4m3_b128(const uint8_t *a, int64_t lda, const float *sa, int6
  *   `type`, each with its own stride; each may be NULL (not written), and may be
  *   its own columns of x (in place: same pointer and stride).
  * n_q, n_kv 0 .. 1024; head_dim even, 2 .. 256; 1 <= n_pairs <= head_dim / 2; 1 <= n_axes <= 8.
- * Pointers and strides need only their element's alignment; rows on 16-byte
- * boundaries with head_dim and n_pairs multiples of 8 run with 16-byte
- * accesses. */
+ * Pointers and strides need only their element's alignment; a thread moves 8,
+ * 4, 2 or 1 elements at a time, the most that head_dim, n_pairs and the rows'
+ * alignment allow. */
 fm_status fm_rope_axes(const void *x, fm_dtype type, int64_t ldx, int rows, int n_q, int n_kv,
                        int head_dim, const int32_t *positions, int64_t ldp, int n_axes,
                        const uint8_t *pair_axis, const double *pair_freq, int n_pairs, void *q_out,

@@ -227,63 +227,83 @@ __device__ __forceinline__ float gated(float g, float u) {
   return g * r * u;
 }
 
-template <typename T, int ACT>
+// U rows per thread, their loads in flight together.
+template <typename T, int ACT, int U>
 __global__ void __launch_bounds__(256) gated_kernel(const GatedParams p) {
   grid_dep_launch();
   grid_dep_wait();
   const int lane = threadIdx.x & 31;
   int64_t row;
-  int c;
+  int c, stride = 1;
   bool live = true;
   if (p.tiles) {
-    row = blockIdx.x / (unsigned)p.tiles;
+    row = (int64_t)(blockIdx.x / (unsigned)p.tiles) * U;
     c = (blockIdx.x % (unsigned)p.tiles) * blockDim.x + threadIdx.x;
   } else {
     const int slot = threadIdx.x / p.row_pieces;     // the block's threads are rounded up to whole warps
     live = slot < p.rpb;
-    row = (int64_t)blockIdx.x * p.rpb + slot;
+    row = (int64_t)blockIdx.x * p.rpb * U + slot;
     c = threadIdx.x - slot * p.row_pieces;
+    stride = p.rpb;
   }
-  live = live && row < p.rows && c * 8 < p.f;
-  float y[8];
-  if (live) {
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx + (int64_t)c * 8;
-    Pack8<T> a, b;
-    a.load(x);
-    if (ACT != FM_ACT_NONE) b.load(x + p.f);
-    a.get(y);
-    if (ACT != FM_ACT_NONE) {
-      float u[8];
-      b.get(u);
+  live = live && c * 8 < p.f;
+  const T* x = static_cast<const T*>(p.x) + row * p.ldx + (int64_t)c * 8;
+  Pack8<T> a[U], b[U];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = gated<ACT>(y[e], u[e]);
+  for (int u = 0; u < U; ++u) {
+    if (live && row + u * stride < p.rows) {
+      a[u].load(x + (int64_t)u * stride * p.ldx);
+      if (ACT != FM_ACT_NONE) b[u].load(x + (int64_t)u * stride * p.ldx + p.f);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = 0.f;
   }
-  quantize_group(y, live, lane, p.codes + row * p.ldc + (int64_t)c * 8, p.scales + row * p.lds + (c >> 4));
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t r = row + u * stride;
+    const bool mine = live && r < p.rows;
+    float y[8];
+    if (mine) {
+      a[u].get(y);
+      if (ACT != FM_ACT_NONE) {
+        float v[8];
+        b[u].get(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = gated<ACT>(y[e], v[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = 0.f;
+    }
+    quantize_group(y, mine, lane, p.codes + r * p.ldc + (int64_t)c * 8, p.scales + r * p.lds + (c >> 4));
+  }
 }
 
-template <typename T>
-cudaError_t launch_gated(GatedParams p, fm_act act, cudaStream_t st) {
-  p.row_pieces = ((p.f + 127) / 128) * 16;
+template <typename T, int U>
+cudaError_t launch_gated_u(GatedParams p, fm_act act, cudaStream_t st) {
   int threads = 256;
   int64_t grid;
   if (p.row_pieces >= 256) {
     p.tiles = (p.row_pieces + 255) / 256;
     p.rpb = 0;
-    grid = (int64_t)p.rows * p.tiles;
+    grid = ((int64_t)p.rows + U - 1) / U * p.tiles;
   } else {
     p.tiles = 0;
     p.rpb = 256 / p.row_pieces;
     threads = (p.rpb * p.row_pieces + 31) & ~31;
-    grid = ((int64_t)p.rows + p.rpb - 1) / p.rpb;
+    grid = ((int64_t)p.rows + p.rpb * U - 1) / (p.rpb * U);
   }
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return act == FM_ACT_SILU        ? launch_op(gated_kernel<T, FM_ACT_SILU>, (unsigned)grid, threads, 0, 1, st, p)
-         : act == FM_ACT_GELU_TANH ? launch_op(gated_kernel<T, FM_ACT_GELU_TANH>, (unsigned)grid, threads, 0, 1, st, p)
-                                   : launch_op(gated_kernel<T, FM_ACT_NONE>, (unsigned)grid, threads, 0, 1, st, p);
+  return act == FM_ACT_SILU        ? launch_op(gated_kernel<T, FM_ACT_SILU, U>, (unsigned)grid, threads, 0, 1, st, p)
+         : act == FM_ACT_GELU_TANH ? launch_op(gated_kernel<T, FM_ACT_GELU_TANH, U>, (unsigned)grid, threads, 0, 1, st, p)
+                                   : launch_op(gated_kernel<T, FM_ACT_NONE, U>, (unsigned)grid, threads, 0, 1, st, p);
+}
+
+template <typename T>
+cudaError_t launch_gated(GatedParams p, fm_act act, int sms, cudaStream_t st) {
+  p.row_pieces = ((p.f + 127) / 128) * 16;
+  // Where there are pieces for several waves of threads, each takes UU of them.
+  constexpr int UU = sizeof(T) == 2 ? 4 : 2;
+  return (int64_t)p.rows * p.row_pieces >= (int64_t)sms * 2048 * UU ? launch_gated_u<T, UU>(p, act, st)
+                                                                    : launch_gated_u<T, 1>(p, act, st);
 }
 
 // ----------------------------------------------------------------- weight quantiser
@@ -333,40 +353,43 @@ struct RopeParams {
   uint8_t axis[kMaxPairs];
 };
 
+// V consecutive elements, 16 or 2 V / 4 V bytes at a time.
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> { using type = uint4; };
+template <>
+struct Word<8> { using type = uint2; };
+template <>
+struct Word<4> { using type = uint32_t; };
+template <>
+struct Word<2> { using type = uint16_t; };
 template <typename T, int V>
-__device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
-  if constexpr (V == 8) {
-    Pack8<T> a;
-    a.load(p);
-    a.get(v);
-  } else {
+struct Run {
+  static constexpr int kBytes = V * (int)sizeof(T), kWord = kBytes < 16 ? kBytes : 16;
+  using W = typename Word<kWord>::type;
+  union {
+    W w[kBytes / kWord];
+    T e[V];
+  };
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = to_f(p[i]);
+    for (int i = 0; i < kBytes / kWord; ++i) w[i] = reinterpret_cast<const W*>(p)[i];
   }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
-  if constexpr (V == 8) {
-    store8(p, v);
-  } else {
+  __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-    for (int i = 0; i < V; ++i) from_f(p + i, v[i]);
+    for (int i = 0; i < kBytes / kWord; ++i) reinterpret_cast<W*>(p)[i] = w[i];
   }
-}
-// V elements as they are.
+};
 template <typename T, int V>
 __device__ __forceinline__ void copy_v(const T* src, T* dst) {
-  if constexpr (V == 8) {
-#pragma unroll
-    for (int i = 0; i < (int)(8 * sizeof(T) / 16); ++i) reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) dst[i] = src[i];
-  }
+  Run<T, V> r;
+  r.load(src);
+  r.store(dst);
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ double turn[kMaxPairs];
   __shared__ uint8_t axis[kMaxPairs];
   grid_dep_launch();
@@ -401,17 +424,18 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
     if (out == nullptr) continue;
     const T* in = x + h * hd;
     out += h * hd;
-    float lo[V], hi[V], a[V], b[V];
-    load_v<T, V>(in + j, lo);
-    load_v<T, V>(in + j + n, hi);
+    Run<T, V> a, b;
+    a.load(in + j);
+    b.load(in + j + n);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      // spelled out, so that both widths round alike
-      a[e] = __fmaf_rn(lo[e], c[e], -__fmul_rn(hi[e], s[e]));
-      b[e] = __fmaf_rn(hi[e], c[e], __fmul_rn(lo[e], s[e]));
+      // spelled out, so that every width rounds alike
+      const float lo = to_f(a.e[e]), hi = to_f(b.e[e]);
+      from_f(&a.e[e], __fmaf_rn(lo, c[e], -__fmul_rn(hi, s[e])));
+      from_f(&b.e[e], __fmaf_rn(hi, c[e], __fmul_rn(lo, s[e])));
     }
-    store_v<T, V>(out + j, a);
-    store_v<T, V>(out + j + n, b);
+    a.store(out + j);
+    b.store(out + j + n);
     for (int e = 2 * n + j; e < hd; e += n) copy_v<T, V>(in + e, out + e);
   }
   if (p.v != nullptr) {
@@ -423,21 +447,24 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
 }
 
 template <typename T>
-cudaError_t launch_rope(RopeParams& p, bool wide, int sms, cudaStream_t st) {
-  const int per = wide ? p.n / 8 : p.n, heads = p.nq + p.nkv;
+cudaError_t launch_rope(RopeParams& p, int v, int sms, cudaStream_t st) {
+  const int per = p.n / v, heads = p.nq + p.nkv;
   // Shares of the heads: enough threads to fill the GPU (1024 per SM), and no
   // more than that, because each share makes the row's cosines and sines again.
   int64_t parts = (int64_t)sms * 1024 / ((int64_t)p.rows * per);
   parts = parts < 1 ? 1 : parts > heads ? heads : parts;
   p.parts = parts < 1 ? 1 : (int)parts;
-  const int64_t grid = ((int64_t)p.rows * p.parts * per + 255) / 256;
+  const int64_t grid = ((int64_t)p.rows * p.parts * per + 127) / 128;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return wide ? launch_op(rope_kernel<T, 8>, (unsigned)grid, 256, 0, 1, st, p)
-              : launch_op(rope_kernel<T, 1>, (unsigned)grid, 256, 0, 1, st, p);
+  return v == 8   ? launch_op(rope_kernel<T, 8>, (unsigned)grid, 128, 0, 1, st, p)
+         : v == 4 ? launch_op(rope_kernel<T, 4>, (unsigned)grid, 128, 0, 1, st, p)
+         : v == 2 ? launch_op(rope_kernel<T, 2>, (unsigned)grid, 128, 0, 1, st, p)
+                  : launch_op(rope_kernel<T, 1>, (unsigned)grid, 128, 0, 1, st, p);
 }
 
-bool mult16(const void* p, int64_t ld, size_t elem, int rows) {
-  return ((uintptr_t)p & 15u) == 0 && (rows <= 1 || ((uint64_t)ld * elem) % 16 == 0);
+// Whether `n` rows at `p` start on `bytes`-byte boundaries (NULL: nothing to ask).
+bool rows_on(size_t bytes, const void* p, int64_t ld, size_t elem, int n) {
+  return p == nullptr || ((uintptr_t)p % bytes == 0 && (n <= 1 || ((uint64_t)ld * elem) % bytes == 0));
 }
 
 }  // namespace
@@ -568,7 +595,9 @@ fm_status fm_gated_e4m3(const void* x, fm_dtype x_type, int64_t ldx, fm_act act,
   FM_TRY(c.memory());
   fm::GatedParams p{x, codes, scales, ldx, ldc, lds, rows, f, 0, 0, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return c.launched(x_type == FM_BF16 ? fm::launch_gated<uint16_t>(p, act, st) : fm::launch_gated<float>(p, act, st));
+  const int sms = fm::sm_count(c.device);
+  return c.launched(x_type == FM_BF16 ? fm::launch_gated<uint16_t>(p, act, sms, st)
+                                      : fm::launch_gated<float>(p, act, sms, st));
 }
 
 fm_status fm_quantize_weight_e4m3_b128(const uint16_t* w, int64_t ldw, int n, int k, uint8_t* codes, int64_t ldc,
@@ -628,12 +657,18 @@ fm_status fm_rope_axes(const void* x, fm_dtype type, int64_t ldx, int rows, int 
   p.x = x; p.pos = positions; p.q = q_out; p.k = k_out; p.v = v_out;
   p.ldx = ldx; p.ldp = ldp; p.ldq = ldq; p.ldk = ldk; p.ldv = ldv;
   p.rows = rows; p.nq = n_q; p.nkv = n_kv; p.hd = head_dim; p.n = n_pairs; p.parts = 1;
-  const bool wide = head_dim % 8 == 0 && n_pairs % 8 == 0 && fm::mult16(x, ldx, es, rows) &&
-                    fm::mult16(q_out, ldq, es, q_out ? rows : 0) && fm::mult16(k_out, ldk, es, k_out ? rows : 0) &&
-                    fm::mult16(v_out, ldv, es, v_out ? rows : 0);
+  // the widest run that divides the pairs and the head and that every row allows
+  int v = 8;
+  for (; v > 1; v /= 2) {
+    const size_t on = v * es < 16 ? v * es : 16;
+    if (head_dim % v == 0 && n_pairs % v == 0 && fm::rows_on(on, x, ldx, es, rows) &&
+        fm::rows_on(on, q_out, ldq, es, rows) && fm::rows_on(on, k_out, ldk, es, rows) &&
+        fm::rows_on(on, v_out, ldv, es, rows))
+      break;
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int sms = fm::sm_count(c.device);
-  return c.launched(type == FM_BF16 ? fm::launch_rope<uint16_t>(p, wide, sms, st) : fm::launch_rope<float>(p, wide, sms, st));
+  return c.launched(type == FM_BF16 ? fm::launch_rope<uint16_t>(p, v, sms, st) : fm::launch_rope<float>(p, v, sms, st));
 }
 
 #pragma GCC visibility pop

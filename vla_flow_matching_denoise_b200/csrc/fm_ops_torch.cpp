@@ -303,16 +303,32 @@ Heads heads_out(PyObject* o, const char* name, const at::Tensor& x, int64_t rows
   return Heads{t, rows > 1 ? t.stride(0) : heads * hd};
 }
 
-// (x, positions, axis address, freq address, n_pairs, n_q, n_kv, head_dim, q_out, k_out, v_out, stream) -> (q, k, v)
+// A contiguous 1-D buffer of `size`-byte elements of struct format `code`.
+struct View {
+  Py_buffer b;
+  View(PyObject* o, char code, Py_ssize_t size) {
+    const int flags = PyBUF_ND | PyBUF_FORMAT | PyBUF_C_CONTIGUOUS;
+    if (PyObject_GetBuffer(o, &b, flags) != 0) throw python_error();
+    if (b.ndim != 1 || b.itemsize != size || b.format == nullptr || b.format[0] != code || b.format[1] != 0) {
+      PyBuffer_Release(&b);
+      bad("pairs must be (uint8 [n], float64 [n]) contiguous arrays (see rope_pairs)");
+    }
+  }
+  View(const View&) = delete;
+  ~View() { PyBuffer_Release(&b); }
+  Py_ssize_t size() const { return b.shape[0]; }
+};
+
+// (x, positions, axis, freq, n_q, n_kv, head_dim, q_out, k_out, v_out, stream) -> (q, k, v)
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  ENTRY(12)
+  ENTRY(11)
   const at::Tensor& x = tensor(a[0], "x");
-  const Scope scope(x, a[11]);
+  const Scope scope(x, a[10]);
   const int64_t ldx = matrix(x, "x", kReal, nullptr), rows = x.size(0);
-  const int n_pairs = as_int(a[4]), n_q = as_int(a[5]), n_kv = as_int(a[6]), hd = as_int(a[7]);
+  const int n_q = as_int(a[4]), n_kv = as_int(a[5]), hd = as_int(a[6]);
   if (n_q < 0 || n_kv < 0 || hd < 1 || n_q > 1024 || n_kv > 1024 || hd > 256)
     bad("n_q %d / n_kv %d / head_dim %d out of range (0 .. 1024 heads of 2 .. 256)", n_q, n_kv, hd);
-  const bool with_v = a[10] != Py_False;
+  const bool with_v = a[9] != Py_False;
   const int64_t want = (int64_t)(n_q + (with_v ? 2 : 1) * n_kv) * hd;
   if (x.size(1) < want || (with_v && x.size(1) != want)) bad("x has %lld columns, expected %lld", (long long)x.size(1), (long long)want);
   const at::Tensor& pos = tensor(a[1], "positions");
@@ -326,15 +342,14 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     ldp = matrix(pos, "positions", kInt, &x, -1, rows);
     axes = pos.size(0);
   }
-  Heads q = heads_out(a[8], "q_out", x, rows, n_q, hd), k = heads_out(a[9], "k_out", x, rows, n_kv, hd),
-        v = heads_out(a[10], "v_out", x, rows, n_kv, hd);
-  const auto* axis = (const uint8_t*)PyLong_AsVoidPtr(a[2]);
-  const auto* freq = (const double*)PyLong_AsVoidPtr(a[3]);
-  if (PyErr_Occurred()) throw python_error();
+  Heads q = heads_out(a[7], "q_out", x, rows, n_q, hd), k = heads_out(a[8], "k_out", x, rows, n_kv, hd),
+        v = heads_out(a[9], "v_out", x, rows, n_kv, hd);
+  const View axis(a[2], 'B', 1), freq(a[3], 'd', 8);
+  if (axis.size() != freq.size() || axis.size() > 256) bad("pairs: %lld axes and %lld frequencies", (long long)axis.size(), (long long)freq.size());
   auto at_ = [](const Heads& h) { return h.t.defined() ? ptr(h.t) : nullptr; };
   run("fm_rope_axes", x, [&](void* st) {
-    return fm_rope_axes(ptr(x), dtype_of(x), ldx, (int)rows, n_q, n_kv, hd, (const int32_t*)ptr(pos), ldp, (int)axes, axis, freq,
-                        n_pairs, at_(q), q.ld, at_(k), k.ld, at_(v), v.ld, st);
+    return fm_rope_axes(ptr(x), dtype_of(x), ldx, (int)rows, n_q, n_kv, hd, (const int32_t*)ptr(pos), ldp, (int)axes, (const uint8_t*)axis.b.buf,
+                        (const double*)freq.b.buf, (int)axis.size(), at_(q), q.ld, at_(k), k.ld, at_(v), v.ld, st);
   });
   auto back = [](PyObject* o, const Heads& h) {
     if (o == Py_False) o = Py_None;
@@ -342,7 +357,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     Py_INCREF(o);
     return o;
   };
-  return pack({back(a[8], q), back(a[9], k), back(a[10], v)});
+  return pack({back(a[7], q), back(a[8], k), back(a[9], v)});
   LEAVE
 }
 

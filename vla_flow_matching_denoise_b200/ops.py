@@ -120,11 +120,7 @@ def rope_axes(x, positions, pairs, n_q: int, n_kv: int, head_dim: int, *, q_out=
     columns of x for an update in place), or None where False is given.  With
     v_out=False x may end after the key heads."""
     axis, freq = pairs
-    if axis.dtype != np.uint8 or freq.dtype != np.float64 or axis.ndim != 1 or axis.shape != freq.shape \
-            or not axis.flags.c_contiguous or not freq.flags.c_contiguous:
-        raise ValueError("pairs must be (uint8 [n], float64 [n]) contiguous arrays (see rope_pairs)")
-    return _ops.rope(x, positions, axis.ctypes.data, freq.ctypes.data, axis.shape[0], n_q, n_kv, head_dim, q_out, k_out,
-                     v_out, _handle(stream))
+    return _ops.rope(x, positions, axis, freq, n_q, n_kv, head_dim, q_out, k_out, v_out, _handle(stream))
 
 
 def sync(stream=None) -> None:
