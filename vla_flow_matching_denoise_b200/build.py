@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libfm_expert.so")
 OPS = os.path.join(PKG, "_ops.so")
 SOURCES = ["fm_api.cu", "fm_prep.cu", "fm_time.cu", "fm_step.cu", "fm_batch.cu", "fm_attn.cu", "fm_noalloc.cu",
            "fm_ops.cu", "fm_ops_gemm.cu"]
-HEADERS = ["fm_internal.h", "fm_batch.h", "fm_launch.h", "fm_ptx.cuh", "fm_ops_check.h"]
+HEADERS = ["fm_internal.h", "fm_batch.h", "fm_launch.h", "fm_ptx.cuh", "fm_ops_check.h", "fm_ops_math.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -13,6 +13,7 @@
 
 #include "../../include/fm_ops.h"
 #include "fm_ops_check.h"
+#include "fm_ops_math.cuh"
 #include "fm_ptx.cuh"
 
 namespace fm {
@@ -62,29 +63,70 @@ __device__ __forceinline__ void from_f(uint16_t* p, float v) {
 }
 __device__ __forceinline__ void from_f(float* p, float v) { *p = v; }
 
-// ----------------------------------------------------------------- group of 128 -> codes + scale
-// Half a warp holds one group of 128 values, 8 per lane (`live` false: none, the
-// group's ragged end).  a' = max(a, 2^-100) keeps 448 / a' finite, so tiny
-// groups give codes and not 0 x inf.
+// ----------------------------------------------------------------- groups of 128 -> codes + scales
+// Half a warp holds one group of 128 values, 8 per lane (a piece), and N such
+// groups at once.  a' = max(a, 2^-100) keeps 448 / a' finite, so tiny groups
+// give codes and not 0 x inf.  The maxima of the N groups are exchanged
+// together (the lane bits 8 and 4 tell whose a lane ends up with), so the two
+// divisions are made once for all N and not once for each: they and the
+// shuffles were a quarter of the instructions of kernels that are bound by them.
 constexpr float kTiny = 7.8886090522101181e-31f;   // 2^-100
-__device__ __forceinline__ void quantize_group(const float (&y)[8], bool live, int lane, uint8_t* code, float* scale) {
-  float a = 0.f;
+template <int N>
+struct Groups {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  float r, s;              // 448 / a' and a' / 448 of group `mine`
+  int mine;
+
+  __device__ __forceinline__ Groups(const float (&y)[N][8], int lane) {
+    float a[N];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(y[i]));
+    for (int i = 0; i < N; ++i) {
+      a[i] = fabsf(y[i][0]);
 #pragma unroll
-  for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-  const float t = fmaxf(a, kTiny);
-  const float r = a > 0.f ? __fdiv_rn(448.0f, t) : 1.0f;
-  if (live) {
-    uint2 c;
-    c.x = f32x2_to_e4m3x2(__fmul_rn(y[0], r), __fmul_rn(y[1], r)) |
-          (f32x2_to_e4m3x2(__fmul_rn(y[2], r), __fmul_rn(y[3], r)) << 16);
-    c.y = f32x2_to_e4m3x2(__fmul_rn(y[4], r), __fmul_rn(y[5], r)) |
-          (f32x2_to_e4m3x2(__fmul_rn(y[6], r), __fmul_rn(y[7], r)) << 16);
-    *reinterpret_cast<uint2*>(code) = c;
-    if ((lane & 15) == 0) *scale = a > 0.f ? __fdiv_rn(t, 448.0f) : 1.0f;
+      for (int e = 1; e < 7; e += 2) a[i] = max_abs3(a[i], y[i][e], y[i][e + 1]);
+      a[i] = fmaxf(a[i], fabsf(y[i][7]));
+    }
+    float m;
+    int o = 8;
+    mine = 0;
+    if constexpr (N == 4) {
+      const bool hi = lane & 8;
+      const float s0 = hi ? a[0] : a[2], s1 = hi ? a[1] : a[3];
+      a[0] = fmaxf(hi ? a[2] : a[0], __shfl_xor_sync(0xffffffffu, s0, 8));
+      a[1] = fmaxf(hi ? a[3] : a[1], __shfl_xor_sync(0xffffffffu, s1, 8));
+      mine = hi ? 2 : 0;
+      o = 4;
+    }
+    if constexpr (N >= 2) {
+      const bool hi = lane & o;
+      const float send = hi ? a[0] : a[1];
+      m = fmaxf(hi ? a[1] : a[0], __shfl_xor_sync(0xffffffffu, send, o));
+      mine += hi ? 1 : 0;
+      o >>= 1;
+    } else {
+      m = a[0];
+    }
+    for (; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float t = fmaxf(m, kTiny);
+    r = m > 0.f ? __fdiv_rn(448.0f, t) : 1.0f;
+    s = m > 0.f ? __fdiv_rn(t, 448.0f) : 1.0f;
   }
-}
+  // Whether this lane is the one that stores the scale of group `mine`.
+  static __device__ __forceinline__ bool writer(int lane) { return (lane & (N == 4 ? 3 : N == 2 ? 7 : 15)) == 0; }
+  // 448 / a' of group i, for every lane (all lanes call it).
+  __device__ __forceinline__ float factor(int i, int lane) const {
+    if constexpr (N == 1) return r;
+    const int src = (lane & 16) | (N == 4 ? ((i >> 1) << 3) | ((i & 1) << 2) : i << 3);
+    return __shfl_sync(0xffffffffu, r, src);
+  }
+  // The codes of a piece of group i.
+  static __device__ __forceinline__ uint2 codes(float (&y)[8], float f) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) mul2(y[e], y[e + 1], f, f);
+    return make_uint2(f32x2_to_e4m3x2(y[0], y[1]) | (f32x2_to_e4m3x2(y[2], y[3]) << 16),
+                      f32x2_to_e4m3x2(y[4], y[5]) | (f32x2_to_e4m3x2(y[6], y[7]) << 16));
+  }
+};
 
 // ----------------------------------------------------------------- residual + RMS norm
 // A row stays in the registers of its `wpr` warps between the sum of squares
@@ -116,7 +158,7 @@ __global__ void norm_kernel(const NormParams p) {
   const TH* res = static_cast<const TH*>(p.res) + row * p.ldr;
 
   float v[NP][8];
-  float sq = 0.f;
+  float sq = 0.f, sq1 = 0.f;
   {
     Pack8<TX> px[NP];
     Pack8<TH> pr[NP];
@@ -137,17 +179,18 @@ __global__ void norm_kernel(const NormParams p) {
           float r[8];
           pr[i].get(r);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][e] += r[e];
+          for (int e = 0; e < 8; e += 2) add2(v[i][e], v[i][e + 1], r[e], r[e + 1]);
         }
         if (p.h != nullptr) store8(static_cast<TH*>(p.h) + row * p.ldh + c * 8, v[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sq = fmaf(v[i][e], v[i][e], sq);
+        for (int e = 0; e < 8; e += 2) fma2(sq, sq1, v[i][e], v[i][e + 1], v[i][e], v[i][e + 1]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
       }
     }
   }
+  sq += sq1;
 #pragma unroll
   for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
   if (p.wpr > 1) {
@@ -160,20 +203,35 @@ __global__ void norm_kernel(const NormParams p) {
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int c = t + i * step;
-    if (i * step >= pieces) break;                            // the same for every lane
-    const bool live = have && c < pieces;
-    float g[8];
-    if (p.gain != nullptr && live) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) mul2(v[i][e], v[i][e + 1], rstd, rstd);
+    if (p.gain != nullptr) {
       Pack8<uint16_t> pg;
-      pg.load(p.gain + c * 8);
+      float g[8];
+      pg.r = make_uint4(0, 0, 0, 0);
+      if (c < pieces) pg.load(p.gain + c * 8);
       pg.get(g);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        add2(g[e], g[e + 1], p.offset, p.offset);
+        mul2(v[i][e], v[i][e + 1], g[e], g[e + 1]);
+      }
     } else {
+      const float g = 1.f + p.offset;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = 1.f;
+      for (int e = 0; e < 8; e += 2) mul2(v[i][e], v[i][e + 1], g, g);
     }
+  }
+  const Groups<NP> groups(v, lane);
+  if (have) {
+    const int first = (t & ~15) + groups.mine * step;          // the group's first piece
+    if (Groups<NP>::writer(lane) && first < pieces) p.scales[row * p.lds + (first >> 4)] = groups.s;
+  }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * rstd * (g[e] + p.offset);
-    quantize_group(v[i], live, lane, p.codes + row * p.ldc + c * 8, p.scales + row * p.lds + (c >> 4));
+  for (int i = 0; i < NP; ++i) {
+    const int c = t + i * step;
+    const uint2 code = Groups<NP>::codes(v[i], groups.factor(i, lane));
+    if (have && c < pieces) *reinterpret_cast<uint2*>(p.codes + row * p.ldc + c * 8) = code;
   }
 }
 
@@ -212,19 +270,26 @@ struct GatedParams {
 // true division the kernel was bound by instructions (96 us at 16384 x 4096,
 // memory 52).  An overflow of the exponential gives 1/inf = 0, the limit.
 template <int ACT>
-__device__ __forceinline__ float gated(float g, float u) {
+__device__ __forceinline__ void gated2(float& g0, float& g1, float u0, float u1) {
   constexpr float kLog2e = 1.4426950408889634f;
-  float t;   // -t log2(e)
+  float t0 = g0, t1 = g1;   // -t log2(e)
   if (ACT == FM_ACT_SILU) {
-    t = -kLog2e * g;
+    mul2(t0, t1, -kLog2e, -kLog2e);
   } else {
     constexpr float c = -2.0f * 0.7978845608028654f * kLog2e;
-    t = g * fmaf(c * 0.044715f, g * g, c);
+    float w0 = c, w1 = c;
+    mul2(t0, t1, g0, g1);
+    fma2(w0, w1, t0, t1, c * 0.044715f, c * 0.044715f);
+    t0 = g0, t1 = g1;
+    mul2(t0, t1, w0, w1);
   }
-  float e, r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return g * r * u;
+  asm("ex2.approx.f32 %0, %0;" : "+f"(t0));
+  asm("ex2.approx.f32 %0, %0;" : "+f"(t1));
+  add2(t0, t1, 1.0f, 1.0f);
+  asm("rcp.approx.f32 %0, %0;" : "+f"(t0));
+  asm("rcp.approx.f32 %0, %0;" : "+f"(t1));
+  mul2(g0, g1, t0, t1);
+  mul2(g0, g1, u0, u1);
 }
 
 // U rows per thread, their loads in flight together.
@@ -256,24 +321,32 @@ __global__ void __launch_bounds__(256) gated_kernel(const GatedParams p) {
       if (ACT != FM_ACT_NONE) b[u].load(x + (int64_t)u * stride * p.ldx + p.f);
     }
   }
+  float y[U][8];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t r = row + u * stride;
-    const bool mine = live && r < p.rows;
-    float y[8];
-    if (mine) {
-      a[u].get(y);
+    if (live && row + u * stride < p.rows) {
+      a[u].get(y[u]);
       if (ACT != FM_ACT_NONE) {
         float v[8];
         b[u].get(v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = gated<ACT>(y[e], v[e]);
+        for (int e = 0; e < 8; e += 2) gated2<ACT>(y[u][e], y[u][e + 1], v[e], v[e + 1]);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = 0.f;
+      for (int e = 0; e < 8; ++e) y[u][e] = 0.f;
     }
-    quantize_group(y, mine, lane, p.codes + r * p.ldc + (int64_t)c * 8, p.scales + r * p.lds + (c >> 4));
+  }
+  const Groups<U> groups(y, lane);
+  if (live) {
+    const int64_t r = row + groups.mine * stride;
+    if (Groups<U>::writer(lane) && r < p.rows) p.scales[r * p.lds + (c >> 4)] = groups.s;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t r = row + u * stride;
+    const uint2 code = Groups<U>::codes(y[u], groups.factor(u, lane));
+    if (live && r < p.rows) *reinterpret_cast<uint2*>(p.codes + r * p.ldc + (int64_t)c * 8) = code;
   }
 }
 

@@ -19,6 +19,7 @@
 
 #include "../../include/fm_ops.h"
 #include "fm_ops_check.h"
+#include "fm_ops_math.cuh"
 #include "fm_ptx.cuh"
 
 namespace fm {
@@ -60,15 +61,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-// (c0, c1) += (a0, a1) * (b0, b1): one instruction for two fp32 FMAs.
-__device__ __forceinline__ void fma2(float& c0, float& c1, float a0, float a1, float b0, float b1) {
-  asm("{\n\t.reg .b64 a, b, c;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%0, %1};\n\t"
-      "fma.rn.f32x2 c, a, b, c;\n\t"
-      "mov.b64 {%0, %1}, c;\n\t}"
-      : "+f"(c0), "+f"(c1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
