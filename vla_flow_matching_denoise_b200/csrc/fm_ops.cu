@@ -410,10 +410,10 @@ __global__ void __launch_bounds__(256) quantize_weight_kernel(const uint16_t* __
 }
 
 // ----------------------------------------------------------------- multi-axis RoPE
-// A thread owns V consecutive pairs of one row and walks over heads with their
-// cosines and sines in registers, so they are made once for all heads of its
-// share; few rows split the heads over more threads instead.  The angle is
-// reduced to a fraction of a turn in 64 bits (positions x frequency pass 2^20
+// A block takes whole rows, so that what is in flight is contiguous, and makes
+// their cosines and sines once, in shared memory, while its loads are on the
+// way: a thread owns V consecutive pairs of kHeads heads of one row.  The angle
+// is reduced to a fraction of a turn in 64 bits (positions x frequency pass 2^20
 // turns, where fp32 has no digits left).
 constexpr int kMaxPairs = 128;
 struct RopeParams {
@@ -421,7 +421,8 @@ struct RopeParams {
   const int32_t* pos;
   void *q, *k, *v;
   int64_t ldx, ldp, ldq, ldk, ldv;
-  int rows, nq, nkv, hd, n, parts;    // parts: shares of the heads
+  int rows, nq, nkv, hd, n;
+  int parts, tb;                      // shares of the heads; rows per block
   double turn[kMaxPairs];             // frequency in turns per position
   uint8_t axis[kMaxPairs];
 };
@@ -461,8 +462,10 @@ __device__ __forceinline__ void copy_v(const T* src, T* dst) {
   r.store(dst);
 }
 
+constexpr int kHeads = 3;
 template <typename T, int V>
-__global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ float4 table[];
   __shared__ double turn[kMaxPairs];
   __shared__ uint8_t axis[kMaxPairs];
   grid_dep_launch();
@@ -472,67 +475,97 @@ __global__ void __launch_bounds__(128) rope_kernel(const __grid_constant__ RopeP
   }
   __syncthreads();
   grid_dep_wait();
-  const int per = p.n / V;                                    // threads per row and share
-  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t slot = id / per;
-  const int j = (int)(id - slot * per) * V;
-  const int64_t row = slot / p.parts;
-  const int part = (int)(slot - row * p.parts);
-  if (row >= p.rows) return;
-  float c[V], s[V];
+  const int n = p.n, hd = p.hd, heads = p.nq + p.nkv;
+  const int per = n / V;                                      // threads per row and share of the heads
+  const int slot = (int)threadIdx.x / per, j = ((int)threadIdx.x - slot * per) * V;
+  const int r = slot / p.parts, part = slot - r * p.parts;
+  const int vals = p.v != nullptr ? p.nkv * hd : 0, ve = part * n + j;    // this thread's first value element
+  const int size = (p.tb * n + 3) & ~3;
+  int buf = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * p.tb; row0 < p.rows; row0 += (int64_t)gridDim.x * p.tb, buf ^= 1) {
+    const int here = (int)(p.rows - row0 < p.tb ? p.rows - row0 : p.tb);
+    const bool mine = r < here;
+    const int64_t row = row0 + (mine ? r : 0);
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    T* q = static_cast<T*>(p.q);
+    T* k = static_cast<T*>(p.k);
+    if (q != nullptr) q += row * p.ldq;
+    if (k != nullptr) k += row * p.ldk - (int64_t)p.nq * hd;
+    Run<T, V> a[kHeads], b[kHeads], v;
+    auto bring = [&](int h0) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    const double a = (double)p.pos[(int64_t)axis[j + e] * p.ldp + row] * turn[j + e];
-    sincospif(2.0f * (float)(a - rint(a)), &s[e], &c[e]);
-  }
-  const int heads = p.nq + p.nkv, n = p.n, hd = p.hd;
-  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-  T* q = static_cast<T*>(p.q);
-  T* k = static_cast<T*>(p.k);
-  if (q != nullptr) q += row * p.ldq;
-  if (k != nullptr) k += row * p.ldk - (int64_t)p.nq * hd;
-#pragma unroll 4
-  for (int h = part; h < heads; h += p.parts) {
-    T* out = h < p.nq ? q : k;
-    if (out == nullptr) continue;
-    const T* in = x + h * hd;
-    out += h * hd;
-    Run<T, V> a, b;
-    a.load(in + j);
-    b.load(in + j + n);
+      for (int u = 0; u < kHeads; ++u) {
+        const int h = h0 + u * p.parts;
+        if (h < heads && (h < p.nq ? q : k) != nullptr) {
+          a[u].load(x + h * hd + j);
+          b[u].load(x + h * hd + j + n);
+        }
+      }
+    };
+    if (mine) bring(part);
+    if (mine && ve < vals) v.load(x + heads * hd + ve);
+    float* cs = reinterpret_cast<float*>(table) + buf * 2 * size;          // [tb][n] cosines, then the sines
+    for (int i = threadIdx.x; i < here * n; i += blockDim.x) {
+      const int w = i / n, e = i - w * n;
+      const double z = (double)p.pos[(int64_t)axis[e] * p.ldp + row0 + w] * turn[e];
+      sincospif(2.0f * (float)(z - rint(z)), &cs[size + i], &cs[i]);
+    }
+    __syncthreads();                                          // (the other buffer's readers are one barrier behind)
+    if (!mine) continue;
+    float c[V], s[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      // spelled out, so that every width rounds alike
-      const float lo = to_f(a.e[e]), hi = to_f(b.e[e]);
-      from_f(&a.e[e], __fmaf_rn(lo, c[e], -__fmul_rn(hi, s[e])));
-      from_f(&b.e[e], __fmaf_rn(hi, c[e], __fmul_rn(lo, s[e])));
+      c[e] = cs[r * n + j + e];
+      s[e] = cs[size + r * n + j + e];
     }
-    a.store(out + j);
-    b.store(out + j + n);
-    for (int e = 2 * n + j; e < hd; e += n) copy_v<T, V>(in + e, out + e);
-  }
-  if (p.v != nullptr) {
-    const T* in = x + heads * hd;
-    T* out = static_cast<T*>(p.v) + row * p.ldv;
-    const int step = p.parts * n;
-    for (int e = part * n + j; e < p.nkv * hd; e += step) copy_v<T, V>(in + e, out + e);
+    auto turn_head = [&](int h, Run<T, V>& lo_, Run<T, V>& hi_) {
+      T* out = (h < p.nq ? q : k) + h * hd;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        // spelled out, so that every width rounds alike
+        const float lo = to_f(lo_.e[e]), hi = to_f(hi_.e[e]);
+        from_f(&lo_.e[e], __fmaf_rn(lo, c[e], -__fmul_rn(hi, s[e])));
+        from_f(&hi_.e[e], __fmaf_rn(hi, c[e], __fmul_rn(lo, s[e])));
+      }
+      lo_.store(out + j);
+      hi_.store(out + j + n);
+      for (int e = 2 * n + j; e < hd; e += n) copy_v<T, V>(x + h * hd + e, out + e);
+    };
+    for (int h0 = part; h0 < heads; h0 += kHeads * p.parts) {
+      if (h0 != part) bring(h0);
+#pragma unroll
+      for (int u = 0; u < kHeads; ++u) {
+        const int h = h0 + u * p.parts;
+        if (h < heads && (h < p.nq ? q : k) != nullptr) turn_head(h, a[u], b[u]);
+      }
+    }
+    T* vo = static_cast<T*>(p.v) + row * p.ldv;
+    if (ve < vals) v.store(vo + ve);
+    for (int e = ve + p.parts * n; e < vals; e += p.parts * n) copy_v<T, V>(x + heads * hd + e, vo + e);
   }
 }
 
 template <typename T>
 cudaError_t launch_rope(RopeParams& p, int v, int sms, cudaStream_t st) {
   const int per = p.n / v, heads = p.nq + p.nkv;
-  // Shares of the heads: enough threads to fill the GPU (1024 per SM), and no
-  // more than that, because each share makes the row's cosines and sines again.
-  int64_t parts = (int64_t)sms * 1024 / ((int64_t)p.rows * per);
-  parts = parts < 1 ? 1 : parts > heads ? heads : parts;
+  // one head per thread where rows are few, kHeads or a few times that where
+  // they fill the GPU; whole rows up to about 128 threads per block
+  int64_t parts = ((int64_t)sms * 1536 + (int64_t)p.rows * per - 1) / ((int64_t)p.rows * per);
+  const int64_t most_parts = (int64_t)p.rows * per * heads < (int64_t)sms * 1024 ? heads : (heads + kHeads - 1) / kHeads;
+  if (parts > most_parts) parts = most_parts;
+  if (parts * per > 512) parts = 512 / per;
   p.parts = parts < 1 ? 1 : (int)parts;
-  const int64_t grid = ((int64_t)p.rows * p.parts * per + 127) / 128;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return v == 8   ? launch_op(rope_kernel<T, 8>, (unsigned)grid, 128, 0, 1, st, p)
-         : v == 4 ? launch_op(rope_kernel<T, 4>, (unsigned)grid, 128, 0, 1, st, p)
-         : v == 2 ? launch_op(rope_kernel<T, 2>, (unsigned)grid, 128, 0, 1, st, p)
-                  : launch_op(rope_kernel<T, 1>, (unsigned)grid, 128, 0, 1, st, p);
+  p.tb = 128 / (p.parts * per);
+  if (p.tb < 1) p.tb = 1;
+  if ((int64_t)p.rows < (int64_t)p.tb * sms) p.tb = 1;
+  const int threads = (p.tb * p.parts * per + 31) & ~31;
+  const int64_t tiles = ((int64_t)p.rows + p.tb - 1) / p.tb, most = (int64_t)sms * (2048 / threads);
+  const int64_t grid = tiles < most ? tiles : most;
+  const size_t smem = 4 * (size_t)((p.tb * p.n + 3) & ~3) * sizeof(float);   // at most 128 pairs twice, or one row
+  return v == 8   ? launch_op(rope_kernel<T, 8>, (unsigned)grid, threads, smem, 1, st, p)
+         : v == 4 ? launch_op(rope_kernel<T, 4>, (unsigned)grid, threads, smem, 1, st, p)
+         : v == 2 ? launch_op(rope_kernel<T, 2>, (unsigned)grid, threads, smem, 1, st, p)
+                  : launch_op(rope_kernel<T, 1>, (unsigned)grid, threads, smem, 1, st, p);
 }
 
 // Whether `n` rows at `p` start on `bytes`-byte boundaries (NULL: nothing to ask).
@@ -729,7 +762,7 @@ fm_status fm_rope_axes(const void* x, fm_dtype type, int64_t ldx, int rows, int 
   FM_TRY(c.memory());
   p.x = x; p.pos = positions; p.q = q_out; p.k = k_out; p.v = v_out;
   p.ldx = ldx; p.ldp = ldp; p.ldq = ldq; p.ldk = ldk; p.ldv = ldv;
-  p.rows = rows; p.nq = n_q; p.nkv = n_kv; p.hd = head_dim; p.n = n_pairs; p.parts = 1;
+  p.rows = rows; p.nq = n_q; p.nkv = n_kv; p.hd = head_dim; p.n = n_pairs; p.parts = p.tb = 1;
   // the widest run that divides the pairs and the head and that every row allows
   int v = 8;
   for (; v > 1; v /= 2) {
