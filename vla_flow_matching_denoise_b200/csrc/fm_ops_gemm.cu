@@ -659,27 +659,31 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
       // the warp's rows, 128 bytes of them at a time (64 bf16 or 32 fp32
       // columns), as 16-byte pieces swizzled by (row & 7)
       const int sw7 = lane & 7;
-      auto flush = [&](int half, int c0, int width) {      // slot `half` holds columns c0 .. c0 + width - 1
+      auto flush = [&](int c0, int width) {                // the slots hold columns c0 .. c0 + 2 width - 1
         if (tma_out) {
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && ok && row0 < p.m && c0 < p.n) {
-            tma_store_2d(&mo, c0, row0, smem_u32(stage + half * C::kSlot));
+          if (lane == 0) {
+            if (ok && row0 < p.m && c0 < p.n) tma_store_2d(&mo, c0, row0, smem_u32(stage));
+            if (ok && row0 < p.m && c0 + width < p.n) tma_store_2d(&mo, c0 + width, row0, smem_u32(stage + C::kSlot));
+            bulk_commit_group();
           }
-          if (lane == 0) bulk_commit_group();
         } else {
           __syncwarp();
           const int per = width / 32;                      // 2 bf16 or 1 fp32 per lane and row
           for (int r = 0; r < 32 && row0 + r < p.m && ok; ++r) {
-            const uint32_t word = *reinterpret_cast<const uint32_t*>(stage + half * C::kSlot + r * 128 +
-                                                                     (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-            const int j = c0 + lane * per;
-            if (per == 1) {
-              if (j < p.n) static_cast<float*>(p.out)[(int64_t)(row0 + r) * p.ldo + j] = __uint_as_float(word);
-            } else {
-              uint16_t* o = static_cast<uint16_t*>(p.out) + (int64_t)(row0 + r) * p.ldo + j;
-              if (j < p.n) o[0] = (uint16_t)word;
-              if (j + 1 < p.n) o[1] = (uint16_t)(word >> 16);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t word = *reinterpret_cast<const uint32_t*>(stage + half * C::kSlot + r * 128 +
+                                                                       (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+              const int j = c0 + half * width + lane * per;
+              if (per == 1) {
+                if (j < p.n) static_cast<float*>(p.out)[(int64_t)(row0 + r) * p.ldo + j] = __uint_as_float(word);
+              } else {
+                uint16_t* o = static_cast<uint16_t*>(p.out) + (int64_t)(row0 + r) * p.ldo + j;
+                if (j < p.n) o[0] = (uint16_t)word;
+                if (j + 1 < p.n) o[1] = (uint16_t)(word >> 16);
+              }
             }
           }
           __syncwarp();
@@ -687,33 +691,29 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
       };
       if (tma_out && lane == 0) bulk_wait_read();          // the previous tile's slots have been read
       __syncwarp();
+      uint8_t* o = stage + lane * 128;
       if (p.f32) {
 #pragma unroll
-        for (int part = 0; part < 4; ++part) {
-          if (part == 2) {
+        for (int part = 0; part < 2; ++part) {
+          if (part == 1) {
             if (tma_out && lane == 0) bulk_wait_read();
             __syncwarp();
           }
-          uint8_t* o = stage + (part & 1) * C::kSlot + lane * 128;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float* a = acc + part * 32 + k * 4;
-            *reinterpret_cast<float4*>(o + ((k ^ sw7) << 4)) = make_float4(a[0], a[1], a[2], a[3]);
+          for (int k = 0; k < 16; ++k) {
+            const float* a = acc + part * 64 + k * 4;
+            *reinterpret_cast<float4*>(o + (k >> 3) * C::kSlot + (((k & 7) ^ sw7) << 4)) = make_float4(a[0], a[1], a[2], a[3]);
           }
-          flush(part & 1, col0 + part * 32, 32);
+          flush(col0 + part * 64, 32);
         }
       } else {
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          uint8_t* o = stage + part * C::kSlot + lane * 128;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float* a = acc + part * 64 + k * 8;
-            *reinterpret_cast<uint4*>(o + ((k ^ sw7) << 4)) =
-                make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
-          }
-          flush(part, col0 + part * 64, 64);
+        for (int k = 0; k < 16; ++k) {
+          const float* a = acc + k * 8;
+          *reinterpret_cast<uint4*>(o + (k >> 3) * C::kSlot + (((k & 7) ^ sw7) << 4)) =
+              make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
         }
+        flush(col0, 64);
       }
     }
     if (tma_out && lane == 0) bulk_wait_all();
