@@ -4,6 +4,11 @@ their definitions in 64 bits, through the Python binding.
 Tolerances count roundings (u = 2^-24, half a step of fp32; a code is within
 half an E4M3 step of the scaled value) and were set before the first run; each
 is derived where it is used."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 
@@ -19,6 +24,7 @@ if not torch.cuda.is_available():
 from vla_flow_matching_denoise_b200 import ops  # noqa: E402
 from vla_flow_matching_denoise_b200.binding import Expert, FmError, load  # noqa: E402
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 U = 2.0 ** -24
 BF, F32, FP8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
@@ -348,6 +354,19 @@ def test_gemm_non_finite_values_stay_in_their_row_and_column(m):
     assert torch.equal(out[~bad], clean[~bad])
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 300001, 128), (3, 200000, 32), (700, 4099, 144), (3000, 901, 1168), (259, 40000, 96)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gemm_wide_and_odd(m, n, k, dtype):
+    """Many channels of few rows, odd rows of a large output, bias, a short last group."""
+    a, sa, w, sw, bias = _operands(m, n, k, m + n)
+    out = ops.gemm_e4m3(a, sa, w, sw, bias=bias, out_dtype=dtype)
+    ops.sync()
+    for j in range(0, n, 50048):                # a multiple of 128
+        e = min(n, j + 50048)
+        ref, mag = _gemm_ref(a, sa, w[j:e], sw[j // 128:(e + 127) // 128], bias[j:e])
+        assert torch.all((out[:, j:e].double() - ref).abs() <= _gemm_tol(ref, mag, k, dtype))
+
+
 def test_gemm_scales_of_every_size():
     m, n, k = 40, 260, 512
     a, sa, w, sw, _ = _operands(m, n, k, 13)
@@ -649,3 +668,69 @@ def test_given_stream():
         got = ops.gemm_e4m3(a2, sa2, *ins["wq"], stream=s)
         ops.sync(s)
         assert torch.equal(got, want)
+
+
+_FIRST = """
+import torch
+from vla_flow_matching_denoise_b200 import ops
+g = torch.Generator(device="cuda").manual_seed(1)
+x = torch.randn(640, 2048, generator=g, device="cuda").bfloat16()
+w = (torch.randn(4096, 1024, generator=g, device="cuda") * 0.05).bfloat16()
+pos = torch.zeros(3, 640, dtype=torch.int32, device="cuda")
+pairs = ops.rope_pairs((8, 12, 12))
+def run():
+    wc, ws = ops.quantize_weight_e4m3(w)
+    u, su = ops.gated_e4m3(x)
+    h, c, s = ops.add_rmsnorm_e4m3(x)
+    y = ops.gemm_e4m3(u, su, wc, ws)                 # many rows
+    z = ops.gemm_e4m3(u[:5], su[:5], wc, ws)         # few rows
+    q, k, v = ops.rope_axes(y[:, :1024], pos, pairs, 8, 4, 64)
+    return y, z, q, k, v, c.view(torch.uint8)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+want = run()
+ops.sync()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing needs a call before the one that is captured."""
+    r = subprocess.run([sys.executable, "-c", _FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout[-500:] + r.stderr[-1500:]
+
+
+def test_calls_from_several_threads():
+    ins = [_layer_inputs(64 + 8 * i, 20 + i) for i in range(4)]
+    want = [_layer(**i) for i in ins]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(20):
+                got = _layer(**ins[i])
+                st.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    bad.append(i)
+        # a refusal's text belongs to its thread
+        try:
+            ops.gated_e4m3(ins[i]["x"][:, :16 * i + 8].contiguous(), "none")
+        except FmError as e:
+            if f"f {16 * i + 8} out of range" not in str(e):
+                bad.append(str(e))
+        else:
+            bad.append("not refused")
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad

@@ -27,7 +27,13 @@ thread_local std::string g_create_error;
 
 }  // namespace
 
-void fm::set_thread_error(const char* msg) { g_create_error = msg; }
+void fm::set_thread_error(const char* msg) {
+  try {
+    g_create_error = msg;
+  } catch (...) {   // no memory for the text: none, and no exception through a C entry
+    g_create_error.clear();
+  }
+}
 
 namespace {
 

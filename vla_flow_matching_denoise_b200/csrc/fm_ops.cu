@@ -561,7 +561,7 @@ cudaError_t launch_rope(RopeParams& p, int v, int sms, cudaStream_t st) {
   const int threads = (p.tb * p.parts * per + 31) & ~31;
   const int64_t tiles = ((int64_t)p.rows + p.tb - 1) / p.tb, most = (int64_t)sms * (2048 / threads);
   const int64_t grid = tiles < most ? tiles : most;
-  const size_t smem = 4 * (size_t)((p.tb * p.n + 3) & ~3) * sizeof(float);   // at most 128 pairs twice, or one row
+  const size_t smem = 4 * (size_t)((p.tb * p.n + 3) & ~3) * sizeof(float);   // at most 1024 pairs, 16 KB
   return v == 8   ? launch_op(rope_kernel<T, 8>, (unsigned)grid, threads, smem, 1, st, p)
          : v == 4 ? launch_op(rope_kernel<T, 4>, (unsigned)grid, threads, smem, 1, st, p)
          : v == 2 ? launch_op(rope_kernel<T, 2>, (unsigned)grid, threads, smem, 1, st, p)

@@ -392,14 +392,22 @@ cudaError_t launch_few(const CUtensorMap& ma, const CUtensorMap& mw, const GemmP
 // A pair of blocks (cluster of 2, cta_group::2) owns a tile of 256 rows of `a`
 // x 256 output channels: each block brings its own 128 rows and half of the
 // weights (32 KB a group for 128 x 256 x 128 products), which halves the
-// operand traffic a 128 x 256 tile of one block would need.  The leader issues
-// M = 256, N = 128 products, one half of the channels after the other, into
+// operand traffic a 128 x 256 tile of one block would need.  The leader's two
+// MMA warps issue M = 256, N = 128 products, one half of the channels each, into
 // two TMEM accumulators per half; four epilogue warps per half and block
-// scale and sum them, thread = row, so a group's factor is one register.  Half
-// the channels at a time, because an accumulator is given back ~500 cycles after
-// its products end (commit, read, arrive across the pair), as long as the 512
-// cycles a whole group takes: with halves three units are in flight meanwhile.
-// Outputs leave through shared memory, by TMA where `out` allows it.
+// scale and sum them, thread = row, so a group's factor is one register.
+// Outputs leave through shared memory, by TMA where `out` allows it (other
+// rows cost ~4000 cycles a tile more: 38.8 -> 66 us at m 12000, k 512, n 4096
+// -> 4097).
+//
+// What bounds it: a group is 512 cycles of products, but an accumulator comes
+// back only ~1500 cycles after its products are issued (products of both
+// halves, commit, ~390 to read and sum it while the other half's warp shares
+// the scheduler, an arrive across the pair), and TMEM holds two per half: 765
+// cycles a group.  Without the sums the loop takes 557.  Measured and left:
+// one MMA warp for both halves (695 without the sums), N = 256 units (813), 16
+// epilogue warps (870), 32 or 64 columns per load (850, spills).  Under the
+// power cap the clock gives part of it back.
 struct Wide {
   static constexpr int kA = 128 * 128, kB = 64 * 128, kStage = kA + 2 * kB;
   static constexpr int kStages = 5;
@@ -727,12 +735,19 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
   }
 }
 
-// Pairs of blocks that can run at once on the current device.
+// Pairs of blocks of wide_kernel that can run at once on the current device; 0
+// where it cannot run.
 int wide_pairs(int device) {
   static std::atomic<int> known[64];
   if (device >= 0 && device < 64) {
     const int k = known[device].load(std::memory_order_relaxed);
     if (k > 0) return k;
+  }
+  // the register split of wide_kernel needs the registers the launch brings
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, wide_kernel) != cudaSuccess || fa.numRegs * Wide::kThreads < 40 * 128 + 232 * 256) {
+    cudaGetLastError();
+    return 0;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(148);
@@ -759,6 +774,7 @@ cudaError_t launch_wide(const CUtensorMap& ma, const CUtensorMap& mw, const CUte
   if (e != cudaSuccess) return e;
   const int64_t tiles = (((int64_t)p.m + 255) / 256) * (((int64_t)p.n + 255) / 256);
   const int pairs = wide_pairs(device);
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
   const unsigned grid = 2u * (unsigned)(tiles < pairs ? tiles : pairs);
   return launch_op(wide_kernel, grid, Wide::kThreads, Wide::kSmem, 2, st, ma, mw, mo, p, tma_out ? 1 : 0);
 }
