@@ -265,10 +265,12 @@ struct GatedParams {
 
 // act(g) u with both activations as g / (1 + exp(-t)): SiLU has t = g, and
 // (1 + tanh(z)) / 2 = 1 / (1 + exp(-2 z)) makes the tanh form of GELU one with
-// t = 2 z, without its cancellation for negative z.  Two approximate
-// instructions (2^x and 1/x, about 2^-22 each) and six more: with expf and a
-// true division the kernel was bound by instructions (96 us at 16384 x 4096,
-// memory 52).  An overflow of the exponential gives 1/inf = 0, the limit.
+// t = 2 z, without its cancellation for negative z.  2^x and 1/x are the
+// approximate instructions (about 2^-22 each; their forms that keep subnormals
+// take three more instructions each).  Memory bounds it at 16384 x 4096 bf16
+// (52.4 us, the measured copy rate); with expf and a true division, with one
+// row per thread and with subnormals the instructions did (96, 77, 65 us).  An
+// overflow of the exponential gives 1/inf = 0, the limit.
 template <int ACT>
 __device__ __forceinline__ void gated2(float& g0, float& g1, float u0, float u1) {
   constexpr float kLog2e = 1.4426950408889634f;
@@ -283,11 +285,11 @@ __device__ __forceinline__ void gated2(float& g0, float& g1, float u0, float u1)
     t0 = g0, t1 = g1;
     mul2(t0, t1, w0, w1);
   }
-  asm("ex2.approx.f32 %0, %0;" : "+f"(t0));
-  asm("ex2.approx.f32 %0, %0;" : "+f"(t1));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t0));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t1));
   add2(t0, t1, 1.0f, 1.0f);
-  asm("rcp.approx.f32 %0, %0;" : "+f"(t0));
-  asm("rcp.approx.f32 %0, %0;" : "+f"(t1));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t0));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t1));
   mul2(g0, g1, t0, t1);
   mul2(g0, g1, u0, u1);
 }
