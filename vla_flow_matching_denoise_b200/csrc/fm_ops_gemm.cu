@@ -113,6 +113,24 @@ __device__ __forceinline__ void store_out8(const GemmParams& p, int i, int j, co
   }
 }
 
+// As store_out8, of 4 channels (j a multiple of 4).
+__device__ __forceinline__ void store_out4(const GemmParams& p, int i, int j, float4 v) {
+  v.x += bias_at(p, j);
+  v.y += bias_at(p, j + 1);
+  v.z += bias_at(p, j + 2);
+  v.w += bias_at(p, j + 3);
+  const int64_t at = (int64_t)i * p.ldo + j;
+  if (j + 4 > p.n) {
+    store_out1(p, i, j, v.x);
+    store_out1(p, i, j + 1, v.y);
+    store_out1(p, i, j + 2, v.z);
+  } else if (p.f32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  }
+}
+
 // 4 consecutive scales from group g on (0 past the last); `v4`: 16-byte loads allowed.
 __device__ __forceinline__ float4 scales4(const float* s, int g, int groups, bool v4) {
   if (v4 && g + 4 <= groups) return *reinterpret_cast<const float4*>(s + g);
@@ -315,28 +333,34 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
     if (warp >= 2) {
       const float* part = reinterpret_cast<const float*>(ring);
       if (p.vec) {
-        // this rank's share of the tile's rows x 16 pieces of 8 channels
-        const int all = rows * 16, c0 = all * (int)rank / split, c1 = all * ((int)rank + 1) / split;
-        for (int c = c0 + (int)threadIdx.x - 64; c < c1; c += C::kThreads - 64) {
-          const int r = c >> 4, piece = c & 15;
-          const uint32_t at = smem_u32(part + r * 128);
-          const uint32_t lo = at + (((2 * piece) ^ (r & 31)) << 4), hi = at + (((2 * piece + 1) ^ (r & 31)) << 4);
-          float sum[8] = {};
+        // this rank's share of the tile's rows x 32 pieces of 4 channels, four
+        // of them per thread at a time
+        constexpr int kThr = C::kThreads - 64;
+        const int all = rows * 32, c0 = all * (int)rank / split, c1 = all * ((int)rank + 1) / split;
+        const int piece = (int)threadIdx.x & 31, j = n0 + 4 * piece;     // the same for all of a thread's items
+        for (int c = c0 - (c0 & 31) + (int)threadIdx.x - 64; c < c1; c += 4 * kThr) {
+          float4 sum[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (k < split) {
-              const float4 x = ld_dsmem_f4(map_shared_rank(lo, k)), y = ld_dsmem_f4(map_shared_rank(hi, k));
-              sum[0] += x.x;
-              sum[1] += x.y;
-              sum[2] += x.z;
-              sum[3] += x.w;
-              sum[4] += y.x;
-              sum[5] += y.y;
-              sum[6] += y.z;
-              sum[7] += y.w;
+          for (int u = 0; u < 4; ++u) sum[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < split; ++k) {
+            const uint32_t base = map_shared_rank(smem_u32(part), k);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int i = c + u * kThr, r = i >> 5;
+              if (i >= c0 && i < c1) {
+                const float4 x = ld_dsmem_f4(base + r * 512 + ((piece ^ (r & 31)) << 4));
+                sum[u].x += x.x;
+                sum[u].y += x.y;
+                sum[u].z += x.z;
+                sum[u].w += x.w;
+              }
             }
           }
-          store_out8(p, i0 + r, n0 + piece * 8, sum);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int i = c + u * kThr;
+            if (i >= c0 && i < c1) store_out4(p, i0 + (i >> 5), j, sum[u]);
+          }
         }
       } else {
         // rows at any element: a warp takes four rows of this rank's share at a
@@ -781,29 +805,31 @@ cudaError_t launch_wide(const CUtensorMap& ma, const CUtensorMap& mw, const CUte
 
 // Which kernel, how many rows a block brings and how often k is split: the
 // smallest estimated time.  The figures (microseconds) were fitted to sweeps of
-// both kernels over 1 .. 16384 rows, 512 .. 8192 channels and 2 .. 128 groups:
-// a block of few_kernel takes 0.24 a group whatever it holds (one CTA issuing
-// four products and their commits), a pair of wide_kernel 0.45 for four times
-// as much, and adding the sums of a split costs by rows and blocks.
+// both kernels over 1 .. 16384 rows, 16 .. 8192 channels and 1 .. 128 groups,
+// where the choice is within 2 % of the best on average: a block of few_kernel
+// takes 0.24 a group whatever it holds (one MMA warp's four products, waits and
+// commits), a pair of wide_kernel 0.45 for four times as much; adding the sums
+// of a split costs by rows and blocks, and rows of `out` that do not start on
+// 16 bytes cost stores by element.
 struct Choice {
   bool wide;
   int bt, split;
 };
-Choice choose(int64_t m, int64_t n, int64_t groups, int sms) {
+Choice choose(int64_t m, int64_t n, int64_t groups, bool vec, int sms) {
   Choice best{false, m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128, 1};
   const int64_t tiles = (m + best.bt - 1) / best.bt * ((n + 127) / 128);
   const double rows = m < best.bt ? (double)m : best.bt;
   double least = 1e30;
   for (int s = 1; s <= 8 && s <= groups; s *= 2) {
-    // clusters need their blocks on neighbouring SMs: 120 of 148 SMs take clusters of 8
-    const int64_t room = s <= 2 ? sms : s == 4 ? sms * 136 / 148 : sms * 120 / 148;
-    const int64_t waves = (tiles * s + room - 1) / room;
-    const double t = 2.3 + waves * (waves > 1 ? 2.8 + 0.28 * ((groups + s - 1) / s) : 2.0 + 0.24 * ((groups + s - 1) / s)) +
-                     (s > 1 ? 0.1 + rows * (0.014 + 0.003 * s) : 0.0);
+    // clusters need their blocks on neighbouring SMs: 120 of 148 SMs take clusters of 8, 132 of 4
+    const int64_t room = s <= 2 ? sms : s == 4 ? sms * 132 / 148 : sms * 120 / 148;
+    const int64_t waves = (tiles * s + room - 1) / room, g = (groups + s - 1) / s;
+    const double t = (waves > 1 ? 1.5 + waves * (2.8 + 0.28 * g) : 3.3 + 0.24 * g) +
+                     (s > 1 ? 0.1 * s + rows * (0.016 + 0.001 * s) : 0.0) + (vec ? 0.0 : waves * rows * 0.012 / s);
     if (t < least) least = t, best.split = s;
   }
   const int64_t pairs = sms / 2, waves = (((m + 255) / 256) * ((n + 255) / 256) + pairs - 1) / pairs;
-  if (6.0 + waves * (1.1 + 0.45 * groups) < least) best.wide = true;
+  if (4.6 + waves * (1.1 + 0.45 * groups + (vec ? 0.0 : 2.1)) < least) best.wide = true;
   return best;
 }
 
@@ -890,7 +916,7 @@ fm_status fm_gemm_e4m3_b128(const uint8_t* a, int64_t lda, const float* sa, int6
   const size_t es = out_type == FM_F32 ? 4 : 2;
   const bool vec = ((uintptr_t)out & 15) == 0 && (m <= 1 || ((uint64_t)ldo * es) % 16 == 0);
   const fm::GemmParams p{sa, sw, bias, out, ldsa, ldsw, ldo, m, n, (int)groups, out_type == FM_F32, vec};
-  const fm::Choice pick = fm::choose(m, n, (int)groups, fm::sm_count(c.device));
+  const fm::Choice pick = fm::choose(m, n, groups, vec, fm::sm_count(c.device));
   const bool wide = pick.wide;
   const int bt = pick.bt, split = pick.split;
   CUtensorMap ma, mw, mo;
