@@ -467,6 +467,19 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d, uint64_t ad, uint64_t 
       "l"(ad), "l"(bd), "r"(idesc), "n"(ACC)
       : "memory");
 }
+// Whether the phase has completed, without waiting for it (try_wait may sleep
+// for microseconds where it never completes: after the last accumulator).
+__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return r != 0;
+}
 // Arrives on `bar` of both blocks of the pair when this thread's MMAs are done.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
   asm volatile(
@@ -579,7 +592,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
       bool ok = true;
       for (unsigned t = first; ok && t < tiles; t += pairs) {
         for (int g = 0; g < p.groups; ++g) {
-          ok = __all_sync(0xffffffffu, mbar_wait(tempty0 + 8 * b, bph, kSpin) && mbar_wait(full0 + 8 * s, ph, kSpin));
+          ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, ph, kSpin) && mbar_wait(tempty0 + 8 * b, bph, kSpin));
           if (!ok) {
             if (lane == 0) atomicOr(&g_ops_err, 16u);
             break;
@@ -610,27 +623,23 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int q4 = warp & 3, h = warp >> 2;
     const uint32_t ta = tmem + ((uint32_t)(32 * q4) << 16) + h * 256;
-    const uint32_t te0 = leader_addr(smem_u32(&tempty[2 * h])), te1 = leader_addr(smem_u32(&tempty[2 * h + 1]));
-    uint8_t* stage = slots + warp * 2 * C::kSlot;
+    const uint32_t tfull0 = smem_u32(&tfull[2 * h]), te0 = leader_addr(smem_u32(&tempty[2 * h]));
     const bool v4 = (reinterpret_cast<uintptr_t>(p.sa) & 15) == 0 && p.ldsa % 4 == 0;
-    int b = 0, bph = 0, par = 0;
-    bool ok = true;
-    // This row's scales: four groups in hand and four on the way, and the next
-    // channel scale; a tile's first ones are fetched before the tile ahead of it
-    // is written out.
-    float4 fa, fn;
+    uint32_t unit = 0;                         // accumulators used so far: buffer and phase
+    int par = 0;
+    bool ok = true, ready = false;             // ready: the next accumulator was seen
+    // This row's scales of four groups and the next channel scale, fetched a
+    // group ahead (a tile's first ones before the tile ahead of it is written out).
+    float4 fa;
     float wn;
     const float *sa, *sw;
-    int m0, n0;
     auto enter = [&](unsigned t) {
       const TileAt at = tile_at(t, mts, nts);
-      m0 = at.mt * 256 + (int)rank * 128 + 32 * q4;
-      n0 = at.nt * 256 + h * 128;
-      const bool live = m0 + lane < p.m && n0 < p.n;
-      sa = p.sa + (int64_t)(live ? m0 + lane : 0) * p.ldsa;
-      sw = p.sw + (int64_t)(live ? n0 >> 7 : 0) * p.ldsw;
+      const int row = at.mt * 256 + (int)rank * 128 + 32 * q4 + lane, col = at.nt * 256 + h * 128;
+      const bool live = row < p.m && col < p.n;
+      sa = p.sa + (int64_t)(live ? row : 0) * p.ldsa;
+      sw = p.sw + (int64_t)(live ? col >> 7 : 0) * p.ldsw;
       fa = scales4(sa, 0, p.groups, v4);
-      fn = scales4(sa, 4, p.groups, v4);
       wn = sw[0];
     };
     if (first < tiles) enter(first);
@@ -639,42 +648,48 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.f;
       for (int g = 0; g < p.groups; ++g) {
-        const float s = fa.x * wn;
-        if (g + 1 < p.groups) wn = sw[g + 1];
-        if ((g & 3) == 3) {
-          fa = fn;
-          fn = scales4(sa, g + 5, p.groups, v4);
-        } else {
-          fa.x = fa.y;
-          fa.y = fa.z;
-          fa.z = fa.w;
-        }
-        if (!ok) continue;
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tfull[2 * h + b]), bph, kSpin));
+        if (ok && !ready) ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * (unit & 1), (unit >> 1) & 1, kSpin));
         if (!ok) {
           if (lane == 0) atomicOr(&g_ops_err, 32u);
           continue;
         }
         tc_fence_after();
-        float v[2][16];
-        tmem_ld16(ta + b * 128, v[0]);
+        const uint32_t b = unit & 1;
+        ++unit;
+        float v[2][32];
+        tmem_ld32(ta + b * 128, v[0]);
+        const float s = fa.x * wn;
+        if (g + 1 < p.groups) wn = sw[g + 1];
+        if ((g & 3) == 3) {
+          fa = scales4(sa, g + 1, p.groups, v4);
+        } else {
+          fa.x = fa.y;
+          fa.y = fa.z;
+          fa.z = fa.w;
+        }
+        bool next = false;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < 4; ++q) {
           tmem_ld_wait();
-          if (q < 7) {
-            tmem_ld16(ta + b * 128 + (q + 1) * 16, v[(q + 1) & 1]);
-          } else {                               // all read: the accumulator goes back before the last sums
+          if (q < 3) {
+            tmem_ld32(ta + b * 128 + (q + 1) * 32, v[(q + 1) & 1]);
+          } else {
+            // all read: the accumulator goes back before the last sums, and they
+            // cover the look at the next one
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_at(b ? te1 : te0);
+            if (lane == 0) arrive_at(te0 + 8 * b);
+            next = mbar_peek(tfull0 + 8 * (unit & 1), (unit >> 1) & 1);
           }
 #pragma unroll
-          for (int e = 0; e < 16; e += 2)
-            fma2(acc[q * 16 + e], acc[q * 16 + e + 1], v[q & 1][e], v[q & 1][e + 1], s, s);
+          for (int e = 0; e < 32; e += 2)
+            fma2(acc[q * 32 + e], acc[q * 32 + e + 1], v[q & 1][e], v[q & 1][e + 1], s, s);
         }
-        if ((b ^= 1) == 0) bph ^= 1;
+        ready = __all_sync(0xffffffffu, next);
       }
-      const int row0 = m0, col0 = n0;
+      const TileAt here = tile_at(t, mts, nts);
+      const int row0 = here.mt * 256 + (int)rank * 128 + 32 * q4, col0 = here.nt * 256 + h * 128;
+      uint8_t* stage = slots + warp * 2 * C::kSlot;
       if (t + pairs < tiles) enter(t + pairs);
       if (p.bias != nullptr) {
         const int j = col0 + 32 * q4 + lane;
