@@ -628,10 +628,10 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     uint32_t unit = 0;                         // accumulators used so far: buffer and phase
     int par = 0;
     bool ok = true, ready = false;             // ready: the next accumulator was seen
-    // This row's scales of four groups and the next channel scale, fetched a
-    // group ahead (a tile's first ones before the tile ahead of it is written out).
-    float4 fa;
-    float wn;
+    const bool w4 = (reinterpret_cast<uintptr_t>(p.sw) & 15) == 0 && p.ldsw % 4 == 0;
+    // Four groups' scales of this row and of its channels, fetched four groups
+    // ahead (a tile's first ones before the tile ahead of it is written out).
+    float4 fa, fw;
     const float *sa, *sw;
     auto enter = [&](unsigned t) {
       const TileAt at = tile_at(t, mts, nts);
@@ -640,52 +640,51 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
       sa = p.sa + (int64_t)(live ? row : 0) * p.ldsa;
       sw = p.sw + (int64_t)(live ? col >> 7 : 0) * p.ldsw;
       fa = scales4(sa, 0, p.groups, v4);
-      wn = sw[0];
+      fw = scales4(sw, 0, p.groups, w4);
     };
     if (first < tiles) enter(first);
     for (unsigned t = first; t < tiles; t += pairs, par ^= 1) {
       float acc[128];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.f;
-      for (int g = 0; g < p.groups; ++g) {
-        if (ok && !ready) ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * (unit & 1), (unit >> 1) & 1, kSpin));
-        if (!ok) {
-          if (lane == 0) atomicOr(&g_ops_err, 32u);
-          continue;
-        }
-        tc_fence_after();
-        const uint32_t b = unit & 1;
-        ++unit;
-        float v[2][32];
-        tmem_ld32(ta + b * 128, v[0]);
-        const float s = fa.x * wn;
-        if (g + 1 < p.groups) wn = sw[g + 1];
-        if ((g & 3) == 3) {
-          fa = scales4(sa, g + 1, p.groups, v4);
-        } else {
-          fa.x = fa.y;
-          fa.y = fa.z;
-          fa.z = fa.w;
-        }
-        bool next = false;
+      for (int g0 = 0; g0 < p.groups; g0 += 4) {
+        const float s4[4] = {fa.x * fw.x, fa.y * fw.y, fa.z * fw.z, fa.w * fw.w};
+        fa = scales4(sa, g0 + 4, p.groups, v4);
+        fw = scales4(sw, g0 + 4, p.groups, w4);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          tmem_ld_wait();
-          if (q < 3) {
-            tmem_ld32(ta + b * 128 + (q + 1) * 32, v[(q + 1) & 1]);
-          } else {
-            // all read: the accumulator goes back before the last sums, and they
-            // cover the look at the next one
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(te0 + 8 * b);
-            next = mbar_peek(tfull0 + 8 * (unit & 1), (unit >> 1) & 1);
+        for (int u = 0; u < 4; ++u) {
+          if (g0 + u >= p.groups) break;
+          if (ok && !ready) ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * (unit & 1), (unit >> 1) & 1, kSpin));
+          if (!ok) {
+            if (lane == 0) atomicOr(&g_ops_err, 32u);
+            continue;
           }
+          tc_fence_after();
+          const uint32_t b = unit & 1;
+          ++unit;
+          const float s = s4[u];
+          float v[2][32];
+          tmem_ld32(ta + b * 128, v[0]);
+          bool next = false;
 #pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            fma2(acc[q * 32 + e], acc[q * 32 + e + 1], v[q & 1][e], v[q & 1][e + 1], s, s);
+          for (int q = 0; q < 4; ++q) {
+            tmem_ld_wait();
+            if (q < 3) {
+              tmem_ld32(ta + b * 128 + (q + 1) * 32, v[(q + 1) & 1]);
+            } else {
+              // all read: the accumulator goes back before the last sums, and they
+              // cover the look at the next one
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) arrive_at(te0 + 8 * b);
+              next = mbar_peek(tfull0 + 8 * (unit & 1), (unit >> 1) & 1);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              fma2(acc[q * 32 + e], acc[q * 32 + e + 1], v[q & 1][e], v[q & 1][e + 1], s, s);
+          }
+          ready = __all_sync(0xffffffffu, next);
         }
-        ready = __all_sync(0xffffffffu, next);
       }
       const TileAt here = tile_at(t, mts, nts);
       const int row0 = here.mt * 256 + (int)rank * 128 + 32 * q4, col0 = here.nt * 256 + h * 128;
