@@ -62,6 +62,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+// Whether the phase has completed, without waiting for it (try_wait may sleep
+// for microseconds where it never completes: after the last accumulator).
+__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return r != 0;
+}
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -151,7 +164,7 @@ __device__ __forceinline__ float4 scales4(const float* s, int g, int groups, boo
 // nobody reads, and a thread is a row, so a group's factor is one register.
 // (With the channels as the 128-row operand the factors differ by column and
 // come from shared memory, whose bandwidth M = 128, N <= 128 products use up:
-// 830 cycles a group against 370 at 50 rows.)  Each block of the cluster leaves
+// 830 cycles a group against 380 at 50 rows.)  Each block of the cluster leaves
 // its sums in shared memory and adds its share of the tile over all of them in
 // rank order.
 template <int BT>
@@ -204,7 +217,7 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);   // known uniform: TMEM addresses need no moves
   grid_dep_launch();
   grid_dep_wait();                           // everything above touches this block's memory only
   const int g0 = (int)((int64_t)p.groups * rank / split), g1 = (int)((int64_t)p.groups * (rank + 1) / split);
@@ -270,45 +283,43 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
     float acc[64];
 #pragma unroll
     for (int c = 0; c < 64; ++c) acc[c] = 0.f;
-    bool ok = true;
-    // scales of four groups of this row in hand and four on the way
-    float4 fa = scales4(sa, 0, count, v4), fn = scales4(sa, 4, count, v4);
-    float wn = sw[0];
-    uint32_t b = 0, bph = 0;
-    for (int it = 0; it < count; ++it) {
-      const float s = fa.x * wn;
-      if (it + 1 < count) wn = sw[it + 1];
-      if ((it & 3) == 3) {
-        fa = fn;
-        fn = scales4(sa, it + 5, count, v4);
-      } else {
-        fa.x = fa.y;
-        fa.y = fa.z;
-        fa.z = fa.w;
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&tfull[b]), bph, kSpin));
-      if (!ok) {
-        if (lane == 0) atomicOr(&g_ops_err, 4u);
-        break;
-      }
-      tc_fence_after();
-      float v[2][16];
-      tmem_ld16(ta + b * 128, v[0]);
+    const bool w4 = (reinterpret_cast<uintptr_t>(sw) & 15) == 0;
+    const uint32_t tfull0 = smem_u32(tfull), tempty0 = smem_u32(tempty);
+    bool ok = true, ready = false;             // ready: the next accumulator was seen
+    // four groups' scales of this row and of its channels, fetched four groups ahead
+    float4 fa = scales4(sa, 0, count, v4), fw = scales4(sw, 0, count, w4);
+    uint32_t unit = 0;                         // accumulators used so far: buffer and phase
+    static_assert((C::kBufs & (C::kBufs - 1)) == 0, "a power of two");
+    for (int it0 = 0; ok && it0 < count; it0 += 4) {
+      const float s4[4] = {fa.x * fw.x, fa.y * fw.y, fa.z * fw.z, fa.w * fw.w};
+      fa = scales4(sa, it0 + 4, count, v4);
+      fw = scales4(sw, it0 + 4, count, w4);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        tmem_ld_wait();
-        if (q < 3) {
-          tmem_ld16(ta + b * 128 + (q + 1) * 16, v[(q + 1) & 1]);
-        } else {                               // all read: the accumulator goes back
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&tempty[b]));
+      for (int u = 0; u < 4; ++u) {
+        if (it0 + u >= count) break;
+        const uint32_t b = unit % C::kBufs;
+        if (!ready) ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * b, (unit / C::kBufs) & 1, kSpin));
+        if (!ok) {
+          if (lane == 0) atomicOr(&g_ops_err, 4u);
+          break;
         }
+        tc_fence_after();
+        ++unit;
+        const float s = s4[u];
+        float v[2][32];
+        tmem_ld32(ta + b * 128, v[0]);
+        tmem_ld32(ta + b * 128 + 32, v[1]);
+        tmem_ld_wait();
+        // all read: the accumulator goes back, and the sums cover the look at the next
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty0 + 8 * b);
+        const bool next = mbar_peek(tfull0 + 8 * (unit % C::kBufs), (unit / C::kBufs) & 1);
 #pragma unroll
-        for (int e = 0; e < 16; e += 2)
-          fma2(acc[q * 16 + e], acc[q * 16 + e + 1], v[q & 1][e], v[q & 1][e + 1], s, s);
+        for (int e = 0; e < 64; e += 2)
+          fma2(acc[e], acc[e + 1], v[e >> 5][e & 31], v[e >> 5][(e & 31) + 1], s, s);
+        ready = __all_sync(0xffffffffu, next);
       }
-      if (++b == C::kBufs) b = 0, bph ^= 1;
     }
     if (split == 1 && p.vec) {
       if (ok && live) {
@@ -424,14 +435,16 @@ cudaError_t launch_few(const CUtensorMap& ma, const CUtensorMap& mw, const GemmP
 // rows cost ~4000 cycles a tile more: 38.8 -> 66 us at m 12000, k 512, n 4096
 // -> 4097).
 //
-// What bounds it: a group is 512 cycles of products, but an accumulator comes
-// back only ~1500 cycles after its products are issued (products of both
-// halves, commit, ~390 to read and sum it while the other half's warp shares
-// the scheduler, an arrive across the pair), and TMEM holds two per half: 765
-// cycles a group.  Without the sums the loop takes 557.  Measured and left:
-// one MMA warp for both halves (695 without the sums), N = 256 units (813), 16
-// epilogue warps (870), 32 or 64 columns per load (850, spills).  Under the
-// power cap the clock gives part of it back.
+// What bounds it: a group is 512 cycles of products and takes 635 (8192^3 in
+// short runs, 2660 TFLOP/s; 500 us sustained, where the power cap sets the
+// clock and the library's product without group scales takes 420).  The
+// epilogue warps set the pace: two share a scheduler, each reads 128 columns
+// and makes 64 packed FMAs a group, and what they do beside that shows: TMEM
+// addresses that the compiler does not know to be uniform cost 80 cycles, a
+// wait for a barrier that is ready 130, scales fetched group by group 130.
+// Without the sums the loop takes 557.  Measured and left: one MMA warp for
+// both halves (695 without the sums), N = 256 units, 16 epilogue warps (870),
+// 16 columns a load.
 struct Wide {
   static constexpr int kA = 128 * 128, kB = 64 * 128, kStage = kA + 2 * kB;
   static constexpr int kStages = 5;
@@ -466,19 +479,6 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d, uint64_t ad, uint64_t 
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(ad), "l"(bd), "r"(idesc), "n"(ACC)
       : "memory");
-}
-// Whether the phase has completed, without waiting for it (try_wait may sleep
-// for microseconds where it never completes: after the last accumulator).
-__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return r != 0;
 }
 // Arrives on `bar` of both blocks of the pair when this thread's MMAs are done.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
@@ -542,7 +542,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
   __syncthreads();
   cluster_sync_all();                        // both blocks' barriers exist before any remote arrival
   tc_fence_after();
-  const uint32_t tmem = *slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);   // known uniform: TMEM addresses need no moves
   grid_dep_launch();
   grid_dep_wait();                           // everything above touches this pair's memory only
   const unsigned mts = (unsigned)((p.m + 255) / 256), nts = (unsigned)((p.n + 255) / 256);
@@ -820,16 +820,17 @@ cudaError_t launch_wide(const CUtensorMap& ma, const CUtensorMap& mw, const CUte
 // Which kernel, how many rows a block brings and how often k is split: the
 // smallest estimated time.  The figures (microseconds) were fitted to sweeps of
 // both kernels over 1 .. 16384 rows, 16 .. 8192 channels and 1 .. 128 groups,
-// where the choice is within 2 % of the best on average: a block of few_kernel
-// takes 0.24 a group whatever it holds (one MMA warp's four products, waits and
-// commits), a pair of wide_kernel 0.45 for four times as much; adding the sums
-// of a split costs by rows and blocks, and rows of `out` that do not start on
-// 16 bytes cost stores by element.
+// where the choice is within 1 % of the best on average: a block of few_kernel
+// takes 0.20 a group whatever it holds (one MMA warp's four products, waits and
+// commits), a pair of wide_kernel 0.39 for four times as much; adding the sums
+// of a split costs by rows and blocks, rows of `out` that do not start on 16
+// bytes (`vec` false) cost stores by element, and rows of codes that do not
+// start on 128 (`lines` false) two lines of L2 for each 128 codes.
 struct Choice {
   bool wide;
   int bt, split;
 };
-Choice choose(int64_t m, int64_t n, int64_t groups, bool vec, int sms) {
+Choice choose(int64_t m, int64_t n, int64_t groups, bool vec, bool lines, int sms) {
   Choice best{false, m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128, 1};
   const int64_t tiles = (m + best.bt - 1) / best.bt * ((n + 127) / 128);
   const double rows = m < best.bt ? (double)m : best.bt;
@@ -838,12 +839,12 @@ Choice choose(int64_t m, int64_t n, int64_t groups, bool vec, int sms) {
     // clusters need their blocks on neighbouring SMs: 120 of 148 SMs take clusters of 8, 132 of 4
     const int64_t room = s <= 2 ? sms : s == 4 ? sms * 132 / 148 : sms * 120 / 148;
     const int64_t waves = (tiles * s + room - 1) / room, g = (groups + s - 1) / s;
-    const double t = (waves > 1 ? 1.5 + waves * (2.8 + 0.28 * g) : 3.3 + 0.24 * g) +
+    const double t = (waves > 1 ? 1.5 + waves * (2.8 + (lines ? 0.24 : 0.42) * g) : 3.3 + (lines ? 0.20 : 0.38) * g) +
                      (s > 1 ? 0.1 * s + rows * (0.016 + 0.001 * s) : 0.0) + (vec ? 0.0 : waves * rows * 0.012 / s);
     if (t < least) least = t, best.split = s;
   }
   const int64_t pairs = sms / 2, waves = (((m + 255) / 256) * ((n + 255) / 256) + pairs - 1) / pairs;
-  if (4.6 + waves * (1.1 + 0.45 * groups + (vec ? 0.0 : 2.1)) < least) best.wide = true;
+  if (4.6 + waves * (1.1 + 0.39 * groups + (vec ? 0.0 : 2.1)) < least) best.wide = true;
   return best;
 }
 
@@ -930,7 +931,8 @@ fm_status fm_gemm_e4m3_b128(const uint8_t* a, int64_t lda, const float* sa, int6
   const size_t es = out_type == FM_F32 ? 4 : 2;
   const bool vec = ((uintptr_t)out & 15) == 0 && (m <= 1 || ((uint64_t)ldo * es) % 16 == 0);
   const fm::GemmParams p{sa, sw, bias, out, ldsa, ldsw, ldo, m, n, (int)groups, out_type == FM_F32, vec};
-  const fm::Choice pick = fm::choose(m, n, groups, vec, fm::sm_count(c.device));
+  const bool lines = (((uintptr_t)a | (uintptr_t)w) & 127) == 0 && (m <= 1 || lda % 128 == 0) && (n <= 1 || ldw % 128 == 0);
+  const fm::Choice pick = fm::choose(m, n, groups, vec, lines, fm::sm_count(c.device));
   const bool wide = pick.wide;
   const int bt = pick.bt, split = pick.split;
   CUtensorMap ma, mw, mo;
