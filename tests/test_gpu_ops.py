@@ -81,7 +81,8 @@ def _padded(t, extra, fill):
 
 # --------------------------------------------------------------------------- norm
 NORM = [(1, 16), (1, 1024), (3, 128), (2, 2048), (50, 1024), (5, 144), (7, 1008), (306, 2048), (1, 4096), (9, 4112),
-        (2, 8192), (1, 16384), (3, 16368), (513, 1024), (600, 2064), (1025, 496), (520, 16384)]
+        (2, 8192), (1, 16384), (3, 16368), (513, 1024), (600, 2064), (1025, 496), (520, 16384), (4099, 144), (2000, 4112),
+        (6001, 16), (1001, 8208)]
 
 
 def _norm_ref(x, res, gain, offset, eps=1e-6):
@@ -163,7 +164,9 @@ def test_norm_special_rows():
 
 # --------------------------------------------------------------------------- gated
 @pytest.mark.parametrize("rows,f", [(1, 16), (1, 4096), (3, 128), (50, 4096), (5, 144), (33, 1904), (2, 1920), (4, 2048),
-                                    (7, 2064), (129, 11008), (1000, 48), (2, 65536)])
+                                    (7, 2064), (129, 11008), (1000, 48), (2, 65536),
+                                    # several rows per thread, the last group with 1 .. 7 of its 16 pieces
+                                    (2999, 4112), (40001, 144), (80001, 16), (5001, 1968), (9999, 304)])
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh", "none"])
 @pytest.mark.parametrize("xt", [BF, F32])
 def test_gated(rows, f, act, xt):

@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(256) gated_kernel(const GatedParams p) {
     c = threadIdx.x - slot * p.row_pieces;
     stride = p.rpb;
   }
+  const bool group = live && (c & ~15) * 8 < p.f;      // this half warp's group has elements; this lane's piece may not
   live = live && c * 8 < p.f;
   const T* x = static_cast<const T*>(p.x) + row * p.ldx + (int64_t)c * 8;
   Pack8<T> a[U], b[U];
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(256) gated_kernel(const GatedParams p) {
     }
   }
   const Groups<U> groups(y, lane);
-  if (live) {
+  if (group) {
     const int64_t r = row + groups.mine * stride;
     if (Groups<U>::writer(lane) && r < p.rows) p.scales[r * p.lds + (c >> 4)] = groups.s;
   }
