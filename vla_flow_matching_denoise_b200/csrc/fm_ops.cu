@@ -285,12 +285,24 @@ __device__ __forceinline__ void gated2(float& g0, float& g1, float u0, float u1)
     t0 = g0, t1 = g1;
     mul2(t0, t1, w0, w1);
   }
-  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t0));
-  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(t1));
-  add2(t0, t1, 1.0f, 1.0f);
-  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t0));
-  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(t1));
-  mul2(g0, g1, t0, t1);
+  float e0 = t0, e1 = t1;
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e0));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e1));
+  if (ACT == FM_ACT_SILU) {
+    // what t lost to rounding (up to |t| 2^-24 of the exponential): t + l is g
+    // log2(e) to 48 bits and 2^l = 1 + l ln 2.  An overflow stays one.
+    constexpr float kLo = (float)(1.4426950408889634074 - (double)1.4426950408889634f);
+    float l0 = -t0, l1 = -t1;
+    fma2(l0, l1, g0, g1, -kLog2e, -kLog2e);
+    fma2(l0, l1, g0, g1, -kLo, -kLo);
+    mul2(l0, l1, 0.6931471805599453f, 0.6931471805599453f);
+    e0 = fmaf(e0, t0 < 127.f ? l0 : 0.f, e0);
+    e1 = fmaf(e1, t1 < 127.f ? l1 : 0.f, e1);
+  }
+  add2(e0, e1, 1.0f, 1.0f);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e0));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e1));
+  mul2(g0, g1, e0, e1);
   mul2(g0, g1, u0, u1);
 }
 
