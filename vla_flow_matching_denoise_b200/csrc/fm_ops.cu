@@ -290,14 +290,15 @@ __device__ __forceinline__ void gated2(float& g0, float& g1, float u0, float u1)
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e1));
   if (ACT == FM_ACT_SILU) {
     // what t lost to rounding (up to |t| 2^-24 of the exponential): t + l is g
-    // log2(e) to 48 bits and 2^l = 1 + l ln 2.  An overflow stays one.
+    // log2(e) to 48 bits and 2^l = 1 + l ln 2.  Beyond 2^126 there is nothing
+    // to mend: the limits are 0 and g.
     constexpr float kLo = (float)(1.4426950408889634074 - (double)1.4426950408889634f);
     float l0 = -t0, l1 = -t1;
     fma2(l0, l1, g0, g1, -kLog2e, -kLog2e);
     fma2(l0, l1, g0, g1, -kLo, -kLo);
     mul2(l0, l1, 0.6931471805599453f, 0.6931471805599453f);
-    e0 = fmaf(e0, t0 < 127.f ? l0 : 0.f, e0);
-    e1 = fmaf(e1, t1 < 127.f ? l1 : 0.f, e1);
+    e0 = fabsf(t0) < 126.f ? fmaf(e0, l0, e0) : e0;
+    e1 = fabsf(t1) < 126.f ? fmaf(e1, l1, e1) : e1;
   }
   add2(e0, e1, 1.0f, 1.0f);
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e0));
