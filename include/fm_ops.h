@@ -17,8 +17,9 @@
  * Conventions (beside those of fm_expert.h):
  *   * No handle and no workspace: every pointer is the caller's device memory
  *     on the CURRENT device (host memory and memory of another device are
- *     refused), unless marked "host".  Nothing is kept between calls, so calls
- *     on several threads and streams are independent.
+ *     refused), unless marked "host".  Nothing is kept between calls (but the
+ *     error word of fm_ops_sync), so calls on several threads and streams are
+ *     independent.
  *   * Stream-ordered, asynchronous, capturable in a CUDA graph.
  *   * Matrices are row-major; ld* is the distance between rows in elements and
  *     at least the row's width (any value when there is one row or none).
@@ -98,8 +99,9 @@ fm_status fm_quantize_weight_e4m3_b128(const uint16_t *w, int64_t ldw, int n, in
  *   [ceil(n/128), ceil(k/128)]; bias: bf16 [n] or NULL; out: [m, n].
  * k: a multiple of 16, at least 16 (a and w rows on 16-byte boundaries); m
  * and n any.  sa, sw, bias and out need only their element's alignment.  The
- * result does not depend on anything but the operands (fixed summation
- * order).  A device-side wait that exceeds its bound leaves its
+ * same call gives the same bits; where k is split between blocks (and so the
+ * order of the fp32 sums over the groups) is chosen by m, n, k and the
+ * alignment of a, w and out.  A device-side wait that exceeds its bound leaves its
  * part of `out` unspecified and is reported by fm_ops_sync. */
 fm_status fm_gemm_e4m3_b128(const uint8_t *a, int64_t lda, const float *sa, int64_t ldsa,
                             const uint8_t *w, int64_t ldw, const float *sw, int64_t ldsw,

@@ -328,7 +328,7 @@ def test_gemm_exact(m, n, k):
 def test_gemm_strides_and_guards(m, n, k, dtype):
     """Every operand strided inside a buffer of NaN: nothing outside is read or written."""
     a, sa, w, sw, bias = _operands(m, n, k, 11)
-    want = ops.gemm_e4m3(a, sa, w, sw, bias=bias, out_dtype=dtype)
+    ref, mag = _gemm_ref(a, sa, w, sw, bias)
     a2, _ = _padded(a, 48, 0x7F)
     w2, _ = _padded(w, 16, 0x7F)
     sa2, _ = _padded(sa, 1, float("nan"))
@@ -338,7 +338,7 @@ def test_gemm_strides_and_guards(m, n, k, dtype):
     obuf = torch.full((m + 2, n + 7), 7.0, device="cuda", dtype=dtype)
     out = obuf[1:m + 1, 3:n + 3]                # rows at odd element offsets
     got = ops.gemm_e4m3(a2, sa2, w2, sw2, bias=b2[1:n + 1], out=out)
-    assert got is out and torch.equal(out, want)
+    assert got is out and torch.all((out.double() - ref).abs() <= _gemm_tol(ref, mag, k, dtype))
     assert torch.all(obuf[0] == 7) and torch.all(obuf[m + 1:] == 7)
     assert torch.all(obuf[:, :3] == 7) and torch.all(obuf[:, n + 3:] == 7)
 

@@ -58,7 +58,7 @@ def _build_ops(force: bool) -> None:
            "-isystem", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include"),
            "-o", OPS + ".tmp", src, "-L", PKG, "-l:libfm_expert.so", "-Wl,-rpath,$ORIGIN",
-           "-L", os.path.join(t, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+           "-L", os.path.join(t, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -96,7 +97,7 @@ const at::Tensor* bf16_vector(PyObject* o, const char* name, const at::Tensor& l
 fm_dtype dtype_of(const at::Tensor& t) { return t.scalar_type() == at::kFloat ? FM_F32 : FM_BF16; }
 int64_t groups(int64_t cols) { return (cols + 127) / 128; }
 at::Tensor empty(at::IntArrayRef size, const at::Tensor& like, at::ScalarType type) {
-  return at::empty(size, like.options().dtype(type).requires_grad(false));
+  return at::detail::empty_cuda(size, type, like.device(), std::nullopt);
 }
 
 // An output matrix: the one given, or a new one.
