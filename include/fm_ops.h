@@ -134,6 +134,24 @@ fm_status fm_rope_axes(const void *x, fm_dtype type, int64_t ldx, int rows, int 
  * timeout of fm_gemm_e4m3_b128 on the current device. */
 fm_status fm_ops_sync(void *stream);
 
+/* Test hook for failure detection: in the fm_gemm_e4m3_b128 calls that this
+ * thread makes from now on (graphs keep what they were captured with) `role`
+ * gives up when it has done `group` groups of 128 inputs, and every other wait
+ * of the pipeline after `spin_cycles` SM clock cycles (0: the default of about
+ * 2 s).  Such a call ends early where it has more groups than that: its `out` is
+ * unspecified and fm_ops_sync reports FM_ERR_TIMEOUT; the device context stays
+ * usable.  The roles are the loading and the multiplying warps of a cluster's
+ * first and second block (many rows: the two multiplying warps of a pair).
+ * FM_ERR_INVALID_ARG for another role or a negative number. */
+typedef enum fm_stall {
+  FM_STALL_NONE = 0,
+  FM_STALL_TMA0 = 1,
+  FM_STALL_TMA1 = 2,
+  FM_STALL_MMA0 = 3,
+  FM_STALL_MMA1 = 4
+} fm_stall;
+fm_status fm_ops_test_stall(fm_stall role, int group, long long spin_cycles);
+
 #ifdef __cplusplus
 }
 #endif

@@ -183,3 +183,10 @@ def test_python_checks_refuse_cpu_tensors_and_bad_shapes():
         ops.gated_e4m3(x, "relu")
     with pytest.raises(ValueError, match="CUDA tensor"):
         ops.quantize_weight_e4m3(x)
+
+
+@pytest.mark.parametrize("args", [(5, 0, 0), (-1, 0, 0), (1, -1, 0), (1, 0, -1)])
+def test_the_stall_hook_refuses_what_is_out_of_range(lib, args):
+    assert lib.fm_ops_test_stall(*args) == INVALID
+    assert b"fm_ops_test_stall" in lib.fm_last_error(None)
+    assert lib.fm_ops_test_stall(0, 0, 0) == 0

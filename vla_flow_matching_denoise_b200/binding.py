@@ -36,7 +36,7 @@ EXPORTS = ("fm_expert_create", "fm_set_prefix", "fm_set_prefix_varlen", "fm_set_
            "fm_abi_version",
            # include/fm_ops.h
            "fm_add_rmsnorm_e4m3", "fm_gated_e4m3", "fm_quantize_weight_e4m3_b128", "fm_gemm_e4m3_b128",
-           "fm_rope_axes", "fm_ops_sync")
+           "fm_rope_axes", "fm_ops_sync", "fm_ops_test_stall")
 
 
 class FmConfig(ctypes.Structure):
@@ -118,12 +118,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fm_gemm_e4m3_b128.argtypes = [vp, ll, vp, ll, vp, ll, vp, ll, vp, ip, ip, ip, vp, ip, ll, vp]
     lib.fm_rope_axes.argtypes = [vp, ip, ll, ip, ip, ip, ip, vp, ll, ip, vp, vp, ip, vp, ll, vp, ll, vp, ll, vp]
     lib.fm_ops_sync.argtypes = [vp]
+    lib.fm_ops_test_stall.argtypes = [ip, ip, ctypes.c_longlong]
     for name in ("fm_expert_create", "fm_set_prefix", "fm_denoise", "fm_velocity",
                  "fm_time_modulation", "fm_trace_velocity", "fm_get_fp8_weights", "fm_sync",
                  "fm_test_stall", "fm_trace_batched", "fm_get_geometry", "fm_profile_denoise", "fm_profile_phases", "fm_time_modulation_noalloc",
                  "fm_set_prefix_varlen", "fm_set_prefix_builder", "fm_build_prefix", "fm_get_prefix_kv",
                  "fm_get_nvfp4_weights", "fm_quantize_act_e4m3", "fm_add_rmsnorm_e4m3", "fm_gated_e4m3",
-                 "fm_quantize_weight_e4m3_b128", "fm_gemm_e4m3_b128", "fm_rope_axes", "fm_ops_sync"):
+                 "fm_quantize_weight_e4m3_b128", "fm_gemm_e4m3_b128", "fm_rope_axes", "fm_ops_sync", "fm_ops_test_stall"):
         getattr(lib, name).restype = ip
     _lib = lib
     return lib

@@ -28,7 +28,10 @@ namespace {
 // Device-side timeouts since the last fm_ops_sync on this device.
 __device__ unsigned int g_ops_err;
 
-constexpr long long kSpin = 4000000000ll;       // ~2 s of SM cycles
+// The bound of a wait, in SM cycles (about 2 s).  The pipelines' waits take it
+// from GemmParams::spin (fm_ops_test_stall); the waits at a kernel's end, for
+// what is still on its way to a block's shared memory, always have this one.
+constexpr long long kSpin = 4000000000ll;
 
 struct GemmParams {
   const float *sa, *sw;
@@ -37,7 +40,14 @@ struct GemmParams {
   int64_t ldsa, ldsw, ldo;
   int m, n, groups, f32;
   int vec;                 // rows of `out` start on 16-byte boundaries
+  long long spin;          // bound of the pipeline's waits, cycles
+  int stall;               // 0, or the role (FM_STALL_*) that gives up
+  unsigned stall_at;       //   at this group of its own count
 };
+// The group at which `role` gives up, none: 2^32 - 1.
+__device__ __forceinline__ uint32_t stall_of(const GemmParams& p, int role) {
+  return p.stall == role ? p.stall_at : 0xffffffffu;
+}
 
 // 2-D tiled load of a box of 128-byte rows at (column c0, row c1).
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int c0, int c1, uint32_t bar) {
@@ -90,6 +100,21 @@ __device__ __forceinline__ void mma_e4m3_one(uint32_t d, uint64_t ad, uint64_t b
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(ad), "l"(bd), "r"(idesc), "n"(ACC)
       : "memory");
+}
+// Completes `bytes` of the barrier's expected transactions: those of a copy that
+// was announced and will not be made.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Waits for the last phase below `end` on each of the `depth` (<= 32) barriers
+// from bar0 on that phases 0, 1, ... go round on (a whole warp; a barrier per lane).
+__device__ __forceinline__ void await_last(uint32_t bar0, uint32_t depth, uint32_t end, int lane) {
+  const uint32_t l = (uint32_t)lane;
+  if (l < depth && l < end) {
+    const uint32_t last = end - 1 - (end - 1 - l) % depth;
+    mbar_wait(bar0 + 8 * l, (last / depth) & 1, kSpin);
+  }
+  __syncwarp();
 }
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
@@ -190,8 +215,7 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
   uint64_t* empty = full + C::kStages;
   uint64_t* tfull = empty + C::kStages;  // [kBufs]
   uint64_t* tempty = tfull + C::kBufs;   // [kBufs]
-  uint64_t* drain = tempty + C::kBufs;
-  uint32_t* slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + C::kBufs);
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const unsigned rank = split > 1 ? cluster_rank() : 0, tile = blockIdx.x / (unsigned)split;
   const unsigned rt = (unsigned)((p.m + BT - 1) / BT);
@@ -207,7 +231,6 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
       mbar_init(smem_u32(&tfull[b]), 1);
       mbar_init(smem_u32(&tempty[b]), 2 * quarters);
     }
-    mbar_init(smem_u32(drain), 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -227,10 +250,11 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
   // so that addresses and descriptors live in uniform registers.
   if (warp == 0) {
     const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), ring0 = smem_u32(ring);
+    const int stop = (int)stall_of(p, rank == 0 ? FM_STALL_TMA0 : rank == 1 ? FM_STALL_TMA1 : -1);
     uint32_t s = 0, ph = 1;                  // a fresh barrier's previous phase counts as done
     int it = 0;
     for (; it < count; ++it) {
-      if (!__all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ph, kSpin))) {
+      if (!__all_sync(0xffffffffu, it != stop && mbar_wait(empty0 + 8 * s, ph, p.spin))) {
         if (lane == 0) atomicOr(&g_ops_err, 1u);
         break;
       }
@@ -242,16 +266,16 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
       __syncwarp();
       if (++s == C::kStages) s = 0, ph ^= 1;
     }
-    // every issued copy lands before its memory is used for anything else
-    for (int j = it > C::kStages ? it - C::kStages : 0; j < it; ++j)
-      mbar_wait(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1, kSpin);
+    await_last(full0, C::kStages, (uint32_t)it, lane);   // every issued copy has landed
   } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_e4m3(128, 128);
     const uint64_t d0 = desc_sw128(smem_u32(ring));
     const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), tfull0 = smem_u32(tfull), tempty0 = smem_u32(tempty);
+    const int stop = (int)stall_of(p, rank == 0 ? FM_STALL_MMA0 : rank == 1 ? FM_STALL_MMA1 : -1);
     uint32_t s = 0, ph = 0, b = 0, bph = 1;
-    for (int it = 0; it < count; ++it) {
-      if (!__all_sync(0xffffffffu, mbar_wait(tempty0 + 8 * b, bph, kSpin) && mbar_wait(full0 + 8 * s, ph, kSpin))) {
+    int it = 0;
+    for (; it < count; ++it) {
+      if (!__all_sync(0xffffffffu, it != stop && mbar_wait(tempty0 + 8 * b, bph, p.spin) && mbar_wait(full0 + 8 * s, ph, p.spin))) {
         if (lane == 0) atomicOr(&g_ops_err, 2u);
         break;
       }
@@ -269,9 +293,9 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
       if (++s == C::kStages) s = 0, ph ^= 1;
       if (++b == C::kBufs) b = 0, bph ^= 1;
     }
-    if (elect_one()) mma_commit(smem_u32(drain));   // every MMA is done before TMEM and the ring are given up
-    __syncwarp();
-    mbar_wait(smem_u32(drain), 0, kSpin);
+    // every MMA is done and every commit has arrived before TMEM and the ring are given up
+    await_last(tfull0, C::kBufs, (uint32_t)it, lane);
+    await_last(empty0, C::kStages, (uint32_t)it, lane);
   } else if ((warp & 3) < quarters) {
     const int q4 = warp & 3, h = (warp - 2) >> 2;
     const int row = 32 * q4 + lane;            // TMEM lane: row i0 + row
@@ -298,7 +322,7 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
       for (int u = 0; u < 4; ++u) {
         if (it0 + u >= count) break;
         const uint32_t b = unit % C::kBufs;
-        if (!ready) ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * b, (unit / C::kBufs) & 1, kSpin));
+        if (!ready) ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * b, (unit / C::kBufs) & 1, p.spin));
         if (!ok) {
           if (lane == 0) atomicOr(&g_ops_err, 4u);
           break;
@@ -495,6 +519,48 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// Leaves `value` at `slot` of both blocks and arrives on `ended` of both (a whole warp).
+__device__ __forceinline__ void leave_count(uint32_t* slot, uint32_t value, uint64_t* ended, int lane) {
+  if (lane < 2) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_shared_rank(smem_u32(slot), (uint32_t)lane)), "r"(value)
+                 : "memory");
+    mbar_arrive_cluster(smem_u32(ended), (uint32_t)lane);
+  }
+  __syncwarp();
+}
+// The end of the pair's pipeline, by the TMA warp of each block: returns when no
+// copy and no commit is on its way to this block's shared memory (the leader's:
+// to either ring), so that the blocks may leave after one more cluster barrier.
+// Where waits gave up the roles have stopped at different groups.  Each leaves
+// its count and does nothing more, and what a phase lacks is then made up: the
+// other block's copies on the leader's `full`, the other MMA warp's commits on
+// `empty`.  A stage is used again only after both have gone by, so at most one
+// phase of each barrier is open.
+template <int S, int BYTES>
+__device__ __forceinline__ void pair_end(uint32_t full0, uint32_t empty0, uint32_t tfull0, uint32_t ended,
+                                         const uint32_t* counts, uint32_t rank, int lane) {
+  // (a role may still be waiting out its own bound, and one behind it the next)
+  if (!__all_sync(0xffffffffu, mbar_wait_cluster(ended, 0, 8 * kSpin))) return;
+  const volatile uint32_t* c = counts;
+  const uint32_t i0 = c[0], i1 = c[1], m0 = c[2], m1 = c[3];
+  const uint32_t is = i0 < i1 ? i0 : i1, ib = i0 < i1 ? i1 : i0, ms = m0 < m1 ? m0 : m1, mb = m0 < m1 ? m1 : m0;
+  if (lane == 0) {
+    if (rank == 0)
+      for (uint32_t j = is; j < ib; ++j) {
+        if (i0 > i1)
+          mbar_complete_tx(full0 + 8 * (j % S), BYTES);
+        else
+          mbar_arrive_expect_tx(full0 + 8 * (j % S), BYTES);
+      }
+    for (uint32_t j = ms; j < mb; ++j) mbar_arrive(empty0 + 8 * (j % S));
+  }
+  __syncwarp();
+  if (rank == 0) await_last(full0, S, ib, lane);
+  await_last(empty0, S, mb, lane);
+  await_last(tfull0, 2, m0, lane);
+  await_last(tfull0 + 16, 2, m1, lane);
+}
+
 // Tiles in bands of 8 row tiles, so that the tiles in flight share operands in L2.
 struct TileAt {
   int mt, nt;
@@ -517,8 +583,9 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
   uint64_t* empty = full + C::kStages;
   uint64_t* tfull = empty + C::kStages;      // [half][buffer]
   uint64_t* tempty = tfull + 4;              // [half][buffer], the leader's
-  uint64_t* drain = tempty + 4;              // [half]
-  uint32_t* slot = reinterpret_cast<uint32_t*>(drain + 2);
+  uint64_t* ended = tempty + 4;              // four roles of the pair have left their counts:
+  uint32_t* counts = reinterpret_cast<uint32_t*>(ended + 1);   // groups brought by each block, multiplied by each MMA warp
+  uint32_t* slot = counts + 4;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   if (threadIdx.x == 0) {
@@ -530,8 +597,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
       mbar_init(smem_u32(&tfull[b]), 1);
       mbar_init(smem_u32(&tempty[b]), 8);
     }
-    mbar_init(smem_u32(&drain[0]), 1);
-    mbar_init(smem_u32(&drain[1]), 1);
+    mbar_init(smem_u32(ended), 4);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -553,13 +619,14 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 8) {
       const uint32_t empty0 = smem_u32(empty), full0 = smem_u32(full), ring0 = smem_u32(ring), lead0 = leader_addr(full0);
+      const uint32_t stop = stall_of(p, rank == 0 ? FM_STALL_TMA0 : FM_STALL_TMA1);
       uint32_t it = 0, s = 0, ph = 1;        // a fresh barrier's previous phase counts as done
       bool ok = true;
       for (unsigned t = first; ok && t < tiles; t += pairs) {
         const TileAt at = tile_at(t, mts, nts);
         const int m0 = at.mt * 256 + (int)rank * 128, n0 = at.nt * 256 + (int)rank * 64;
         for (int g = 0; g < p.groups; ++g, ++it) {
-          ok = __all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ph, kSpin));
+          ok = __all_sync(0xffffffffu, it != stop && mbar_wait(empty0 + 8 * s, ph, p.spin));
           if (!ok) {
             if (lane == 0) atomicOr(&g_ops_err, 8u);
             break;
@@ -575,10 +642,8 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
           if (++s == C::kStages) s = 0, ph ^= 1;
         }
       }
-      // the leader sees both blocks' copies land before either may exit
-      if (rank == 0)
-        for (uint32_t j = it > (uint32_t)C::kStages ? it - C::kStages : 0; j < it; ++j)
-          mbar_wait(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1, kSpin);
+      leave_count(counts + rank, it, ended, lane);
+      pair_end<C::kStages, C::kStage>(full0, empty0, smem_u32(tfull), smem_u32(ended), counts, rank, lane);
     } else if (warp < 11 && rank == 0) {
       // The whole warp runs the loop and one elected lane issues, so that the
       // descriptors live in uniform registers: a lone thread spent ~1000 cycles
@@ -588,11 +653,13 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
       const uint64_t d0 = desc_sw128(smem_u32(ring)), w0 = desc_sw128(smem_u32(ring) + C::kA + h * C::kB);
       const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), tfull0 = smem_u32(tfull + 2 * h),
                      tempty0 = smem_u32(tempty + 2 * h), dst0 = tmem + h * 256;
-      uint32_t s = 0, ph = 0, b = 0, bph = 1;
+      const uint32_t stop = stall_of(p, h == 0 ? FM_STALL_MMA0 : FM_STALL_MMA1);
+      uint32_t s = 0, ph = 0, b = 0, bph = 1, it = 0;
       bool ok = true;
       for (unsigned t = first; ok && t < tiles; t += pairs) {
-        for (int g = 0; g < p.groups; ++g) {
-          ok = __all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, ph, kSpin) && mbar_wait(tempty0 + 8 * b, bph, kSpin));
+        for (int g = 0; g < p.groups; ++g, ++it) {
+          ok = __all_sync(0xffffffffu, it != stop && mbar_wait(full0 + 8 * s, ph, p.spin) &&
+                                           mbar_wait(tempty0 + 8 * b, bph, p.spin));
           if (!ok) {
             if (lane == 0) atomicOr(&g_ops_err, 16u);
             break;
@@ -613,11 +680,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
           if ((b ^= 1) == 0) bph ^= 1;
         }
       }
-      if (elect_one())
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain + h))
-                     : "memory");
-      __syncwarp();
-      mbar_wait(smem_u32(drain + h), 0, kSpin);
+      leave_count(counts + 2 + h, it, ended, lane);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -654,7 +717,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           if (g0 + u >= p.groups) break;
-          if (ok && !ready) ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * (unit & 1), (unit >> 1) & 1, kSpin));
+          if (ok && !ready) ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * (unit & 1), (unit >> 1) & 1, p.spin));
           if (!ok) {
             if (lane == 0) atomicOr(&g_ops_err, 32u);
             continue;
@@ -848,6 +911,14 @@ Choice choose(int64_t m, int64_t n, int64_t groups, bool vec, bool lines, int sm
   return best;
 }
 
+// fm_ops_test_stall of the calling thread.
+struct Stall {
+  int role = FM_STALL_NONE;
+  unsigned group = 0;
+  long long spin = kSpin;
+};
+thread_local Stall t_stall;
+
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -930,7 +1001,8 @@ fm_status fm_gemm_e4m3_b128(const uint8_t* a, int64_t lda, const float* sa, int6
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const size_t es = out_type == FM_F32 ? 4 : 2;
   const bool vec = ((uintptr_t)out & 15) == 0 && (m <= 1 || ((uint64_t)ldo * es) % 16 == 0);
-  const fm::GemmParams p{sa, sw, bias, out, ldsa, ldsw, ldo, m, n, (int)groups, out_type == FM_F32, vec};
+  const fm::GemmParams p{sa, sw, bias, out, ldsa, ldsw, ldo, m, n, (int)groups, out_type == FM_F32, vec,
+                         fm::t_stall.spin, (int)fm::t_stall.role, fm::t_stall.group};
   const bool lines = (((uintptr_t)a | (uintptr_t)w) & 127) == 0 && (m <= 1 || lda % 128 == 0) && (n <= 1 || ldw % 128 == 0);
   const fm::Choice pick = fm::choose(m, n, groups, vec, lines, fm::sm_count(c.device));
   const bool wide = pick.wide;
@@ -948,6 +1020,19 @@ fm_status fm_gemm_e4m3_b128(const uint8_t* a, int64_t lda, const float* sa, int6
                     : bt == 32 ? fm::launch_few<32>(ma, mw, p, split, st)
                     : bt == 64 ? fm::launch_few<64>(ma, mw, p, split, st)
                                : fm::launch_few<128>(ma, mw, p, split, st));
+}
+
+fm_status fm_ops_test_stall(fm_stall role, int group, long long spin_cycles) {
+  OpCheck c{"fm_ops_test_stall"};
+  fm::set_thread_error("");
+  if (role < FM_STALL_NONE || role > FM_STALL_MMA1)
+    return c.fail(FM_ERR_INVALID_ARG, "role %d out of range", (int)role);
+  if (group < 0 || spin_cycles < 0)
+    return c.fail(FM_ERR_INVALID_ARG, "group %d / spin_cycles %lld is negative", group, spin_cycles);
+  fm::t_stall.role = role;
+  fm::t_stall.group = (unsigned)group;
+  fm::t_stall.spin = spin_cycles == 0 || spin_cycles > fm::kSpin ? fm::kSpin : spin_cycles;
+  return FM_OK;
 }
 
 fm_status fm_ops_sync(void* stream) {
