@@ -44,9 +44,13 @@ struct GemmParams {
   int stall;               // 0, or the role (FM_STALL_*) that gives up
   unsigned stall_at;       //   at this group of its own count
 };
-// The group at which `role` gives up, none: 2^32 - 1.
-__device__ __forceinline__ uint32_t stall_of(const GemmParams& p, int role) {
-  return p.stall == role ? p.stall_at : 0xffffffffu;
+// How many of its next `count` groups `role` does when it has done `done`: all but
+// where it is to give up.  (Outside the loops over groups: a comparison in them
+// cost 50 cycles a group.)
+__device__ __forceinline__ int groups_of(const GemmParams& p, int role, int count, uint32_t done) {
+  if (p.stall != role) return count;
+  const uint32_t left = p.stall_at > done ? p.stall_at - done : 0;
+  return left < (uint32_t)count ? (int)left : count;
 }
 
 // 2-D tiled load of a box of 128-byte rows at (column c0, row c1).
@@ -250,12 +254,11 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
   // so that addresses and descriptors live in uniform registers.
   if (warp == 0) {
     const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), ring0 = smem_u32(ring);
-    const int stop = (int)stall_of(p, rank == 0 ? FM_STALL_TMA0 : rank == 1 ? FM_STALL_TMA1 : -1);
+    const int end = groups_of(p, rank == 0 ? FM_STALL_TMA0 : rank == 1 ? FM_STALL_TMA1 : -1, count, 0);
     uint32_t s = 0, ph = 1;                  // a fresh barrier's previous phase counts as done
     int it = 0;
-    for (; it < count; ++it) {
-      if (!__all_sync(0xffffffffu, it != stop && mbar_wait(empty0 + 8 * s, ph, p.spin))) {
-        if (lane == 0) atomicOr(&g_ops_err, 1u);
+    for (; it < end; ++it) {
+      if (!__all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ph, p.spin))) {
         break;
       }
       if (elect_one()) {
@@ -266,17 +269,17 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
       __syncwarp();
       if (++s == C::kStages) s = 0, ph ^= 1;
     }
+    if (it < count && lane == 0) atomicOr(&g_ops_err, 1u);
     await_last(full0, C::kStages, (uint32_t)it, lane);   // every issued copy has landed
   } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_e4m3(128, 128);
     const uint64_t d0 = desc_sw128(smem_u32(ring));
     const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), tfull0 = smem_u32(tfull), tempty0 = smem_u32(tempty);
-    const int stop = (int)stall_of(p, rank == 0 ? FM_STALL_MMA0 : rank == 1 ? FM_STALL_MMA1 : -1);
+    const int end = groups_of(p, rank == 0 ? FM_STALL_MMA0 : rank == 1 ? FM_STALL_MMA1 : -1, count, 0);
     uint32_t s = 0, ph = 0, b = 0, bph = 1;
     int it = 0;
-    for (; it < count; ++it) {
-      if (!__all_sync(0xffffffffu, it != stop && mbar_wait(tempty0 + 8 * b, bph, p.spin) && mbar_wait(full0 + 8 * s, ph, p.spin))) {
-        if (lane == 0) atomicOr(&g_ops_err, 2u);
+    for (; it < end; ++it) {
+      if (!__all_sync(0xffffffffu, mbar_wait(tempty0 + 8 * b, bph, p.spin) && mbar_wait(full0 + 8 * s, ph, p.spin))) {
         break;
       }
       tc_fence_after();
@@ -293,6 +296,7 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
       if (++s == C::kStages) s = 0, ph ^= 1;
       if (++b == C::kBufs) b = 0, bph ^= 1;
     }
+    if (it < count && lane == 0) atomicOr(&g_ops_err, 2u);
     // every MMA is done and every commit has arrived before TMEM and the ring are given up
     await_last(tfull0, C::kBufs, (uint32_t)it, lane);
     await_last(empty0, C::kStages, (uint32_t)it, lane);
@@ -619,18 +623,15 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 8) {
       const uint32_t empty0 = smem_u32(empty), full0 = smem_u32(full), ring0 = smem_u32(ring), lead0 = leader_addr(full0);
-      const uint32_t stop = stall_of(p, rank == 0 ? FM_STALL_TMA0 : FM_STALL_TMA1);
       uint32_t it = 0, s = 0, ph = 1;        // a fresh barrier's previous phase counts as done
       bool ok = true;
       for (unsigned t = first; ok && t < tiles; t += pairs) {
         const TileAt at = tile_at(t, mts, nts);
         const int m0 = at.mt * 256 + (int)rank * 128, n0 = at.nt * 256 + (int)rank * 64;
-        for (int g = 0; g < p.groups; ++g, ++it) {
-          ok = __all_sync(0xffffffffu, it != stop && mbar_wait(empty0 + 8 * s, ph, p.spin));
-          if (!ok) {
-            if (lane == 0) atomicOr(&g_ops_err, 8u);
-            break;
-          }
+        const int end = groups_of(p, rank == 0 ? FM_STALL_TMA0 : FM_STALL_TMA1, p.groups, it);
+        int g = 0;
+        for (; g < end; ++g) {
+          if (!__all_sync(0xffffffffu, mbar_wait(empty0 + 8 * s, ph, p.spin))) break;
           if (elect_one()) {
             const uint32_t dst = ring0 + s * C::kStage, bar = lead0 + 8 * s;
             if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * s, 2 * C::kStage);
@@ -641,7 +642,10 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
           __syncwarp();
           if (++s == C::kStages) s = 0, ph ^= 1;
         }
+        it += g;
+        ok = g == p.groups;
       }
+      if (!ok && lane == 0) atomicOr(&g_ops_err, 8u);
       leave_count(counts + rank, it, ended, lane);
       pair_end<C::kStages, C::kStage>(full0, empty0, smem_u32(tfull), smem_u32(ended), counts, rank, lane);
     } else if (warp < 11 && rank == 0) {
@@ -653,17 +657,14 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
       const uint64_t d0 = desc_sw128(smem_u32(ring)), w0 = desc_sw128(smem_u32(ring) + C::kA + h * C::kB);
       const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), tfull0 = smem_u32(tfull + 2 * h),
                      tempty0 = smem_u32(tempty + 2 * h), dst0 = tmem + h * 256;
-      const uint32_t stop = stall_of(p, h == 0 ? FM_STALL_MMA0 : FM_STALL_MMA1);
       uint32_t s = 0, ph = 0, b = 0, bph = 1, it = 0;
       bool ok = true;
       for (unsigned t = first; ok && t < tiles; t += pairs) {
-        for (int g = 0; g < p.groups; ++g, ++it) {
-          ok = __all_sync(0xffffffffu, it != stop && mbar_wait(full0 + 8 * s, ph, p.spin) &&
-                                           mbar_wait(tempty0 + 8 * b, bph, p.spin));
-          if (!ok) {
-            if (lane == 0) atomicOr(&g_ops_err, 16u);
+        const int end = groups_of(p, h == 0 ? FM_STALL_MMA0 : FM_STALL_MMA1, p.groups, it);
+        int g = 0;
+        for (; g < end; ++g) {
+          if (!__all_sync(0xffffffffu, mbar_wait(full0 + 8 * s, ph, p.spin) && mbar_wait(tempty0 + 8 * b, bph, p.spin)))
             break;
-          }
           tc_fence_after();
           if (elect_one()) {
             const uint32_t d = dst0 + b * 128;
@@ -679,7 +680,10 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
           if (++s == C::kStages) s = 0, ph ^= 1;
           if ((b ^= 1) == 0) bph ^= 1;
         }
+        it += g;
+        ok = g == p.groups;
       }
+      if (!ok && lane == 0) atomicOr(&g_ops_err, 16u);
       leave_count(counts + 2 + h, it, ended, lane);
     }
   } else {
