@@ -18,7 +18,7 @@
  *   * No handle and no workspace: every pointer is the caller's device memory
  *     on the CURRENT device (host memory and memory of another device are
  *     refused), unless marked "host".  Nothing is kept between calls (but the
- *     error word of fm_ops_sync), so calls on several threads and streams are
+ *     timeouts that fm_ops_sync reports), so calls on several threads and streams are
  *     independent.
  *   * Stream-ordered, asynchronous, capturable in a CUDA graph.
  *   * Matrices are row-major; ld* is the distance between rows in elements and
@@ -130,8 +130,13 @@ fm_status fm_rope_axes(const void *x, fm_dtype type, int64_t ldx, int rows, int 
                        const uint8_t *pair_axis, const double *pair_freq, int n_pairs, void *q_out,
                        int64_t ldq, void *k_out, int64_t ldk, void *v_out, int64_t ldv, void *stream);
 
-/* Wait for `stream`, then report (FM_ERR_TIMEOUT) and clear any device-side
- * timeout of fm_gemm_e4m3_b128 on the current device. */
+/* Wait for `stream` (of the current device; one that is being captured is
+ * refused), then report (FM_ERR_TIMEOUT) whether any fm_gemm_e4m3_b128 of this
+ * device, on whatever stream, has given up a wait since the calling thread's
+ * previous fm_ops_sync on it (the thread's first: since the library was loaded).
+ * Every thread is told, and told once: after a report the products that the
+ * device ended since the thread's previous call are all in doubt, those of other
+ * streams too. */
 fm_status fm_ops_sync(void *stream);
 
 /* Test hook for failure detection: in the fm_gemm_e4m3_b128 calls that this

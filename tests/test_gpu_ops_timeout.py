@@ -2,6 +2,7 @@
 (fm_ops_test_stall), every other wait runs out its short bound, and the call ends
 by itself, is reported by fm_ops_sync and leaves the device as it was.  No wait
 needs the long bound of a kernel's end: what is in flight there has arrived."""
+import threading
 import time
 
 import pytest
@@ -97,3 +98,56 @@ def test_a_captured_product_that_gives_up():
     del graph, out
     assert torch.equal(ops.gemm_e4m3(*ins), want)
     ops.sync()
+
+
+def _in_thread(f):
+    got = []
+
+    def body():
+        try:
+            got.append(f())
+        except Exception as e:  # noqa: BLE001  (handed to the caller)
+            got.append(e)
+    t = threading.Thread(target=body)
+    t.start()
+    t.join()
+    return got[0]
+
+
+def test_every_thread_is_told():
+    """A report to one thread takes nothing from another, on its own stream or not."""
+    ins = _operands(40, 1000, 2048)
+    ops.sync()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with _Stall(TMA0, 1):
+        ops.gemm_e4m3(*ins, stream=side)
+    first = _in_thread(lambda: ops.sync(side))
+    assert isinstance(first, FmError) and first.status == 5
+    with pytest.raises(FmError, match="gave up"):
+        ops.sync()
+    ops.sync(side)
+    ops.sync(side.cuda_stream)
+
+
+def test_sync_leaves_captures_alone():
+    ins = _operands(40, 1000, 2048)
+    want = ops.gemm_e4m3(*ins)
+    ops.sync()
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(FmError, match="being captured"):
+            ops.sync()                                  # the captured stream itself
+        def elsewhere():
+            try:
+                ops.sync(other)                         # a thread's first: what gave up before is told
+            except FmError as e:
+                assert e.status == 5
+            ops.sync(other)
+        assert _in_thread(elsewhere) is None
+        out = ops.gemm_e4m3(*ins)
+    graph.replay()
+    ops.sync()
+    assert torch.equal(out, want)

@@ -190,3 +190,25 @@ def test_the_stall_hook_refuses_what_is_out_of_range(lib, args):
     assert lib.fm_ops_test_stall(*args) == INVALID
     assert b"fm_ops_test_stall" in lib.fm_last_error(None)
     assert lib.fm_ops_test_stall(0, 0, 0) == 0
+
+
+def test_sync_asks_the_device_of_the_stream(monkeypatch):
+    torch = pytest.importorskip("torch")
+    import contextlib
+    from types import SimpleNamespace
+
+    from vla_flow_matching_denoise_b200 import ops
+    current, asked = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        was, current[0] = current[0], d.index
+        yield
+        current[0] = was
+
+    fake = SimpleNamespace(fm_ops_sync=lambda st: asked.append((current[0], st)) or 0)
+    monkeypatch.setattr(ops, "load", lambda: fake)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    ops.sync(SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=77))
+    ops.sync(78)
+    assert asked == [(1, 77), (0, 78)] and current == [0]

@@ -25,8 +25,13 @@
 namespace fm {
 namespace {
 
-// Device-side timeouts since the last fm_ops_sync on this device.
-__device__ unsigned int g_ops_err;
+// Waits that gave up on this device since the library was loaded: their number
+// (low half; never cleared, so that no reader takes another's report) and which.
+__device__ unsigned long long g_ops_err;
+__device__ __forceinline__ void gave_up(unsigned int which) {
+  atomicOr(&g_ops_err, (unsigned long long)which << 32);
+  atomicAdd(&g_ops_err, 1ull);
+}
 
 // The bound of a wait, in SM cycles (about 2 s).  The pipelines' waits take it
 // from GemmParams::spin (fm_ops_test_stall); the waits at a kernel's end, for
@@ -269,7 +274,7 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
       __syncwarp();
       if (++s == C::kStages) s = 0, ph ^= 1;
     }
-    if (it < count && lane == 0) atomicOr(&g_ops_err, 1u);
+    if (it < count && lane == 0) gave_up(1);
     await_last(full0, C::kStages, (uint32_t)it, lane);   // every issued copy has landed
   } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_e4m3(128, 128);
@@ -296,7 +301,7 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
       if (++s == C::kStages) s = 0, ph ^= 1;
       if (++b == C::kBufs) b = 0, bph ^= 1;
     }
-    if (it < count && lane == 0) atomicOr(&g_ops_err, 2u);
+    if (it < count && lane == 0) gave_up(2);
     // every MMA is done and every commit has arrived before TMEM and the ring are given up
     await_last(tfull0, C::kBufs, (uint32_t)it, lane);
     await_last(empty0, C::kStages, (uint32_t)it, lane);
@@ -328,7 +333,7 @@ few_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUten
         const uint32_t b = unit % C::kBufs;
         if (!ready) ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * b, (unit / C::kBufs) & 1, p.spin));
         if (!ok) {
-          if (lane == 0) atomicOr(&g_ops_err, 4u);
+          if (lane == 0) gave_up(4);
           break;
         }
         tc_fence_after();
@@ -645,7 +650,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         it += g;
         ok = g == p.groups;
       }
-      if (!ok && lane == 0) atomicOr(&g_ops_err, 8u);
+      if (!ok && lane == 0) gave_up(8);
       leave_count(counts + rank, it, ended, lane);
       pair_end<C::kStages, C::kStage>(full0, empty0, smem_u32(tfull), smem_u32(ended), counts, rank, lane);
     } else if (warp < 11 && rank == 0) {
@@ -683,7 +688,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         it += g;
         ok = g == p.groups;
       }
-      if (!ok && lane == 0) atomicOr(&g_ops_err, 16u);
+      if (!ok && lane == 0) gave_up(16);
       leave_count(counts + 2 + h, it, ended, lane);
     }
   } else {
@@ -723,7 +728,7 @@ wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
           if (g0 + u >= p.groups) break;
           if (ok && !ready) ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * (unit & 1), (unit >> 1) & 1, p.spin));
           if (!ok) {
-            if (lane == 0) atomicOr(&g_ops_err, 32u);
+            if (lane == 0) gave_up(32);
             continue;
           }
           tc_fence_after();
@@ -1042,13 +1047,30 @@ fm_status fm_ops_test_stall(fm_stall role, int group, long long spin_cycles) {
 fm_status fm_ops_sync(void* stream) {
   OpCheck c{"fm_ops_sync"};
   fm::set_thread_error("");
-  FM_TRY(c.launched(cudaStreamSynchronize(static_cast<cudaStream_t>(stream))));
-  unsigned int err = 0;
-  FM_TRY(c.launched(cudaMemcpyFromSymbol(&err, fm::g_ops_err, sizeof(err))));
-  if (err == 0) return FM_OK;
-  const unsigned int zero = 0;
-  FM_TRY(c.launched(cudaMemcpyToSymbol(fm::g_ops_err, &zero, sizeof(zero))));
-  return c.fail(FM_ERR_TIMEOUT, "a device-side wait of fm_gemm_e4m3_b128 gave up (code 0x%x)", err);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  FM_TRY(c.launched(cudaStreamIsCapturing(st, &capture)));
+  if (capture != cudaStreamCaptureStatusNone)
+    return c.fail(FM_ERR_INVALID_ARG, "the stream is being captured: there is nothing to wait for");
+  int device = 0;
+  FM_TRY(c.launched(cudaGetDevice(&device)));
+  // the copy goes by `stream`, behind its products; a capture of another thread
+  // is not this call's business
+  unsigned long long word = 0;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  FM_TRY(c.launched(cudaThreadExchangeStreamCaptureMode(&mode)));
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&word, fm::g_ops_err, sizeof(word), 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  FM_TRY(c.launched(e));
+  static thread_local unsigned int seen[64];
+  unsigned int& last = seen[device & 63];
+  const unsigned int count = (unsigned int)word;
+  if (count == last) return FM_OK;
+  const unsigned int fresh = count - last;
+  last = count;
+  return c.fail(FM_ERR_TIMEOUT, "%u device-side waits of fm_gemm_e4m3_b128 gave up (kinds so far 0x%x)", fresh,
+                (unsigned int)(word >> 32));
 }
 
 #pragma GCC visibility pop

@@ -20,6 +20,7 @@ gradients are being recorded.
 """
 from __future__ import annotations
 
+import contextlib
 import os
 from typing import Sequence, Tuple
 
@@ -124,9 +125,14 @@ def rope_axes(x, positions, pairs, n_q: int, n_kv: int, head_dim: int, *, q_out=
 
 
 def sync(stream=None) -> None:
-    """Waits for `stream` (default: the current one) and raises if a device-side
-    wait of gemm_e4m3 gave up since the last call on this device."""
+    """Waits for `stream` (a torch stream, a handle of the current device, or the
+    current stream) and raises if a device-side wait of gemm_e4m3 gave up on the
+    stream's device, whatever stream it ran on, since the calling thread's last
+    sync there: what gemm_e4m3 gave since then is in doubt."""
     lib = load()
-    st = lib.fm_ops_sync(_handle(torch.cuda.current_stream() if stream is None else stream))
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    with contextlib.nullcontext() if isinstance(stream, int) else torch.cuda.device(stream.device):
+        st = lib.fm_ops_sync(_handle(stream))
     if st:
         raise FmError("fm_ops_sync", st, lib.fm_last_error(None).decode())
