@@ -68,7 +68,16 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   const at::Tensor& t = THPVariable_Unpack(o);
   if (!t.is_cuda()) bad("%s must be a CUDA tensor", name);
   if (t.requires_grad() && at::GradMode::is_enabled()) bad("%s requires grad: this operator has no backward", name);
+  if (t._fw_grad(/*level=*/0).defined()) bad("%s carries a forward-mode tangent: this operator has no derivative", name);
   return t;
+}
+
+// A given tensor has been written: a graph that saved it refuses its old values
+// as after any operation in place.
+void written(PyObject* o) {
+  if (o == Py_None || o == Py_False) return;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 // Row stride of a 2-D tensor with unit column stride; rows, cols < 0: any.
@@ -215,6 +224,7 @@ PyObject* add_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return fm_add_rmsnorm_e4m3(ptr(x), dtype_of(x), ldx, ptr(res), ht, ldr, (const uint16_t*)ptr(gain), off, eps, (int)rows,
                                (int)d, h.defined() ? ptr(h) : nullptr, ldh, (uint8_t*)ptr(c.t), c.ld, (float*)ptr(s.t), s.ld, st);
   });
+  for (int i = 5; i < 8; ++i) written(a[i]);
   PyObject* ho;
   if (a[5] == Py_None && h.defined()) {
     ho = give(h);
@@ -244,6 +254,8 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return fm_gated_e4m3(ptr(x), dtype_of(x), ldx, (fm_act)act, (int)rows, (int)f, (uint8_t*)ptr(c.t), c.ld, (float*)ptr(s.t),
                          s.ld, st);
   });
+  written(a[2]);
+  written(a[3]);
   return pack({give_or(a[2], c.t), give_or(a[3], s.t)});
   LEAVE
 }
@@ -283,6 +295,7 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                              (const float*)ptr(sw), ldsw, (const uint16_t*)ptr(bias), (int)m, (int)n, (int)k, ptr(o.t),
                              dtype_of(o.t), o.ld, st);
   });
+  written(a[5]);
   return give_or(a[5], o.t);
   LEAVE
 }
@@ -352,6 +365,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return fm_rope_axes(ptr(x), dtype_of(x), ldx, (int)rows, n_q, n_kv, hd, (const int32_t*)ptr(pos), ldp, (int)axes, (const uint8_t*)axis.b.buf,
                         (const double*)freq.b.buf, (int)axis.size(), at_(q), q.ld, at_(k), k.ld, at_(v), v.ld, st);
   });
+  for (int i = 7; i < 10; ++i) written(a[i]);
   auto back = [](PyObject* o, const Heads& h) {
     if (o == Py_False) o = Py_None;
     else if (o == Py_None) return give(h.t);

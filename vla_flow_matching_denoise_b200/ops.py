@@ -15,8 +15,9 @@ Calls run on the tensors' device, on its current stream (or `stream`), are
 asynchronous and can be captured in a CUDA graph.  Outputs are new tensors
 unless given.  The kernels are in libfm_expert.so, shapes and types are
 checked in _ops.so (csrc/fm_ops_torch.cpp), and a missing library raises.  The
-operators have no backward: an input that requires grad is refused while
-gradients are being recorded.
+operators have no derivative: a tensor that requires grad is refused while
+gradients are being recorded, one with a forward-mode tangent always.  Writing a
+given output counts as an operation in place: a graph that saved it says so.
 """
 from __future__ import annotations
 
