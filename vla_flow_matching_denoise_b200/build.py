@@ -5,7 +5,9 @@
 Output: vla_flow_matching_denoise_b200/libfm_expert.so (C ABI declared in
 include/fm_expert.h and include/fm_ops.h) and _ops.so beside it (the Python
 module that calls include/fm_ops.h on torch tensors; host code only, linked to
-the library).  Rebuilds only what is older than its sources.
+the library).  Rebuilds only what is older than its sources, and _ops.so where
+another Python or torch built it.  Without a CUDA build of torch there is no
+_ops.so; the library and its numpy binding need neither.
 """
 from __future__ import annotations
 
@@ -43,17 +45,33 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _ops_stale(key: str) -> bool:
+    """Whether _ops.so is missing, older than its sources or built for something
+    else than `key` (a text that it holds)."""
+    deps = [os.path.join(CSRC, "fm_ops_torch.cpp"), os.path.join(ROOT, "include", "fm_ops.h"),
+            os.path.join(ROOT, "include", "fm_expert.h"), os.path.abspath(__file__)]
+    if not os.path.exists(OPS) or any(os.path.getmtime(p) > os.path.getmtime(OPS) for p in deps):
+        return True
+    with open(OPS, "rb") as f:
+        return key.encode() + b"\0" not in f.read()
+
+
 def _build_ops(force: bool) -> None:
     """The torch module of the operators (g++, a few headers of torch; needs LIB)."""
-    src = os.path.join(CSRC, "fm_ops_torch.cpp")
-    deps = [src, os.path.join(ROOT, "include", "fm_ops.h"), os.path.join(ROOT, "include", "fm_expert.h"),
-            os.path.abspath(__file__)]
-    if not force and os.path.exists(OPS) and all(os.path.getmtime(p) <= os.path.getmtime(OPS) for p in deps):
+    try:
+        import torch
+    except ImportError:
+        torch = None
+    if torch is None or torch.version.cuda is None:
+        print("no CUDA build of torch: _ops.so (the operators on torch tensors) is not built", file=sys.stderr)
         return
-    import torch
+    key = f"fm_ops for {sys.implementation.cache_tag}, torch {torch.__version__}"
+    if not force and not _ops_stale(key):
+        return
+    src = os.path.join(CSRC, "fm_ops_torch.cpp")
     t = os.path.dirname(os.path.abspath(torch.__file__))
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DFM_OPS_BUILT_FOR="{key}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", os.path.join(t, "include"), "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path()))), "include"),

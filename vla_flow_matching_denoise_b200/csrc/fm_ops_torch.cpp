@@ -383,4 +383,15 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, kMethods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__ops(void) { return PyModule_Create(&kModule); }
+// The Python and torch this was built with; the build looks for it in the file.
+#ifndef FM_OPS_BUILT_FOR
+#define FM_OPS_BUILT_FOR "fm_ops"
+#endif
+PyMODINIT_FUNC PyInit__ops(void) {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", FM_OPS_BUILT_FOR) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -30,8 +30,9 @@ import torch
 
 from .binding import LIB_PATH, FmError, load
 
-if not os.path.exists(LIB_PATH):
-    raise FileNotFoundError(f"{LIB_PATH} is missing: run `python -m vla_flow_matching_denoise_b200.build`")
+for _so in (LIB_PATH, os.path.join(os.path.dirname(LIB_PATH), "_ops.so")):
+    if not os.path.exists(_so):
+        raise FileNotFoundError(f"{_so} is missing: run `python -m vla_flow_matching_denoise_b200.build`")
 from . import _ops  # noqa: E402
 
 _ACT = {"none": 0, "silu": 1, "gelu_tanh": 2}
