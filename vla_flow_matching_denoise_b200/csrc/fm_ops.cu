@@ -108,7 +108,7 @@ struct Groups {
     }
     for (; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float t = fmaxf(m, kTiny);
-    r = m > 0.f ? __fdiv_rn(448.0f, t) : 1.0f;
+    r = m > 0.f ? __fdiv_rn(448.0f, t) : 3e38f;              // (a zero group: any number)
     s = m > 0.f ? __fdiv_rn(t, 448.0f) : 1.0f;
   }
   // Whether this lane is the one that stores the scale of group `mine`.
@@ -270,15 +270,23 @@ struct GatedParams {
 // (1 + tanh(z)) / 2 = 1 / (1 + exp(-2 z)) makes the tanh form of GELU one with
 // t = 2 z, without its cancellation for negative z.  2^x and 1/x are the
 // approximate instructions (about 2^-22 each; their forms that keep subnormals
-// take three more instructions each).  Memory bounds it at 16384 x 4096 bf16
-// (GELU 52.4 us, the measured copy rate; SiLU 55.7 with its exponent to 48
-// bits, 51.6 without); with expf and a true division, with one row per thread
-// and with subnormals the instructions did (96, 77, 65 us).  An overflow of the
-// exponential gives 1/inf = 0, the limit.
+// take three more instructions each).  SiLU's exponent is made to 48 bits: what
+// t loses to rounding, up to |t| 2^-24, is l, and 2^l = 1 + l ln 2.  GELU's comes
+// from three fp32 operations (8 roundings with its constants).  At 16384 x 4096
+// bf16 GELU takes 55.2 us (95 % of the measured copy rate; inputs and outputs that
+// are not in L2), SiLU 57.5; with expf and a true division, with one row per
+// thread and with subnormals it was 96, 77 and 65.
+//
+// Far negative gates, whose 1 / (1 + 2^t) is no normal fp32 number (t > 125: SiLU
+// below -86.6, GELU below -10), come out as 0 or nearly: they are gated_tail's.
+// Their values are below 2^-117 |up|, so that they count only in groups whose
+// largest value is as far below an |up| of theirs: gated_kernel compares the two
+// for each thread and group, and a warp that has such a group makes its rows again
+// (1.3 us of GELU's 55.2, 0.4 of SiLU's; a branch per pair of elements cost 6).
+constexpr float kLog2e = 1.4426950408889634f;
 template <int ACT>
-__device__ __forceinline__ void gated2(float& g0, float& g1, float u0, float u1) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  float t0 = g0, t1 = g1;   // -t log2(e)
+__device__ __forceinline__ void gated_exponent(float g0, float g1, float& t0, float& t1) {   // -t log2(e)
+  t0 = g0, t1 = g1;
   if (ACT == FM_ACT_SILU) {
     mul2(t0, t1, -kLog2e, -kLog2e);
   } else {
@@ -289,27 +297,54 @@ __device__ __forceinline__ void gated2(float& g0, float& g1, float u0, float u1)
     t0 = g0, t1 = g1;
     mul2(t0, t1, w0, w1);
   }
+}
+// l ln 2 for SiLU's exponents t of gates g.
+__device__ __forceinline__ void silu_rest(float g0, float g1, float t0, float t1, float& l0, float& l1) {
+  constexpr float kLo = (float)(1.4426950408889634074 - (double)1.4426950408889634f);
+  l0 = -t0, l1 = -t1;
+  fma2(l0, l1, g0, g1, -kLog2e, -kLog2e);
+  fma2(l0, l1, g0, g1, -kLo, -kLo);
+  mul2(l0, l1, 0.6931471805599453f, 0.6931471805599453f);
+}
+// g u 2^-t (t > 125, where 1 + 2^t is 2^t), 2^-t as two halves so that it may lie
+// below fp32's range where the product does not.
+template <int ACT>
+__device__ __forceinline__ float gated_tail(float g, float u, float t) {
+  float h = -0.5f * t;
+  asm("ex2.approx.f32 %0, %0;" : "+f"(h));
+  float l0 = 0.f, l1 = 0.f;
+  if (ACT == FM_ACT_SILU && h > 0.f) silu_rest(g, g, t, t, l0, l1);
+  const float y = (g * h) * (u * h);
+  return fmaf(-l0, y, y);
+}
+// (g0, g1) = act(g) u, far gates included where TAIL.
+template <int ACT, bool TAIL>
+__device__ __forceinline__ void gated2(float& g0, float& g1, float u0, float u1) {
+  float t0, t1;
+  gated_exponent<ACT>(g0, g1, t0, t1);
   float e0 = t0, e1 = t1;
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e0));
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e1));
   if (ACT == FM_ACT_SILU) {
-    // what t lost to rounding (up to |t| 2^-24 of the exponential): t + l is g
-    // log2(e) to 48 bits and 2^l = 1 + l ln 2.  Beyond 2^126 there is nothing
-    // to mend: the limits are 0 and g.
-    constexpr float kLo = (float)(1.4426950408889634074 - (double)1.4426950408889634f);
-    float l0 = -t0, l1 = -t1;
-    fma2(l0, l1, g0, g1, -kLog2e, -kLog2e);
-    fma2(l0, l1, g0, g1, -kLo, -kLo);
-    mul2(l0, l1, 0.6931471805599453f, 0.6931471805599453f);
+    float l0, l1;
+    silu_rest(g0, g1, t0, t1, l0, l1);
+    // beyond 2^126 there is nothing to mend, and l may be anything: the limits are 0 and g
     e0 = fabsf(t0) < 126.f ? fmaf(e0, l0, e0) : e0;
     e1 = fabsf(t1) < 126.f ? fmaf(e1, l1, e1) : e1;
   }
   add2(e0, e1, 1.0f, 1.0f);
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e0));
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e1));
+  const float far0 = g0, far1 = g1;
   mul2(g0, g1, e0, e1);
   mul2(g0, g1, u0, u1);
+  if (TAIL && t0 > 125.f) g0 = gated_tail<ACT>(far0, u0, t0);
+  if (TAIL && t1 > 125.f) g1 = gated_tail<ACT>(far1, u1, t1);
 }
+
+// A far gate's value is below 2^-117 |up|: its code is 0, and its group's scale is
+// another's, where |up| 448 / a' is below this (2^-10 is half the smallest code).
+constexpr float kTail = 8.1129638414606682e31f;   // 2^106
 
 // U rows per thread, their loads in flight together.
 template <typename T, int ACT, int U>
@@ -341,16 +376,20 @@ __global__ void __launch_bounds__(256) gated_kernel(const GatedParams p) {
       if (ACT != FM_ACT_NONE) b[u].load(x + (int64_t)u * stride * p.ldx + p.f);
     }
   }
-  float y[U][8];
+  float y[U][8], um[U];                               // um: the largest |up| of a piece
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    um[u] = 0.f;
     if (live && row + u * stride < p.rows) {
       a[u].get(y[u]);
       if (ACT != FM_ACT_NONE) {
         float v[8];
         b[u].get(v);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) gated2<ACT>(y[u][e], y[u][e + 1], v[e], v[e + 1]);
+        for (int e = 0; e < 8; e += 2) {
+          um[u] = max_abs3(um[u], v[e], v[e + 1]);
+          gated2<ACT, false>(y[u][e], y[u][e + 1], v[e], v[e + 1]);
+        }
       }
     } else {
 #pragma unroll
@@ -362,11 +401,37 @@ __global__ void __launch_bounds__(256) gated_kernel(const GatedParams p) {
     const int64_t r = row + groups.mine * stride;
     if (Groups<U>::writer(lane) && r < p.rows) p.scales[r * p.lds + (c >> 4)] = groups.s;
   }
+  bool tail = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t r = row + u * stride;
-    const uint2 code = Groups<U>::codes(y[u], groups.factor(u, lane));
+    const float factor = groups.factor(u, lane);
+    const uint2 code = Groups<U>::codes(y[u], factor);
     if (live && r < p.rows) *reinterpret_cast<uint2*>(p.codes + r * p.ldc + (int64_t)c * 8) = code;
+    tail |= um[u] * factor > kTail;
+  }
+  if (ACT != FM_ACT_NONE && __any_sync(0xffffffffu, tail)) {        // rare: x is read again
+#pragma unroll 1
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = row + u * stride;
+      float z[1][8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[0][e] = 0.f;
+      if (live && r < p.rows) {
+        Pack8<T> px;
+        float v[8];
+        px.load(x + (int64_t)u * stride * p.ldx);
+        px.get(z[0]);
+        px.load(x + (int64_t)u * stride * p.ldx + p.f);
+        px.get(v);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) gated2<ACT, true>(z[0][e], z[0][e + 1], v[e], v[e + 1]);
+      }
+      const Groups<1> one(z, lane);
+      if (group && Groups<1>::writer(lane) && r < p.rows) p.scales[r * p.lds + (c >> 4)] = one.s;
+      const uint2 code = Groups<1>::codes(z[0], one.r);
+      if (live && r < p.rows) *reinterpret_cast<uint2*>(p.codes + r * p.ldc + (int64_t)c * 8) = code;
+    }
   }
 }
 
