@@ -70,14 +70,17 @@ typedef enum fm_act {
  *   itself (same pointer and stride), or x itself when the types agree.
  *   codes: [rows, d] bytes; scales: fp32 [rows, ceil(d/128)], any stride.
  * d: a multiple of 16, 16 .. 16384.  eps >= 0 (a zero row with eps = 0 gives
- * NaN). */
+ * NaN).  The sum of squares is fp32: a row whose sum passes 3.4e38 (one h of
+ * 1.9e19) gets zero codes, and with eps = 0 one of |h| below 1e-23 NaN codes. */
 fm_status fm_add_rmsnorm_e4m3(const void *x, fm_dtype x_type, int64_t ldx, const void *residual,
                               fm_dtype h_type, int64_t ldr, const uint16_t *gain, float gain_offset,
                               float eps, int rows, int d, void *h_out, int64_t ldh, uint8_t *codes,
                               int64_t ldc, float *scales, int64_t lds, void *stream);
 
 /* u = act(x[:, :f]) * x[:, f:2f] in fp32 (act FM_ACT_NONE: u = x[:, :f]);
- * codes and scales of u per row and 128 columns.
+ * codes and scales of u per row and 128 columns.  u is good to 13 roundings of
+ * fp32 (GELU's to 8 |t| more, t < 0 its exponent sqrt(8/pi) (gate + 0.044715
+ * gate^3)), far negative gates included.
  *   x: [rows, 2f] (FM_ACT_NONE: [rows, f]) of x_type, gate first.
  *   codes: [rows, f]; scales: fp32 [rows, ceil(f/128)], any stride.
  * f: a multiple of 16, 16 .. 2^20. */
@@ -94,14 +97,15 @@ fm_status fm_quantize_weight_e4m3_b128(const uint16_t *w, int64_t ldw, int n, in
 /* out[i, j] = sum_g sa[i, g] sw[j/128, g] sum_{c in group g} a[i, c] w[j, c]
  *             (+ bias[j]),  groups of 128 consecutive inputs (the last may be
  * shorter).  E4M3 products and fp32 sums inside a group on the tensor cores,
- * fp32 scaling and summing over the groups, one rounding to out_type.
+ * fp32 scaling (by sa sw, rounded to fp32 first: it has to lie in fp32's range)
+ * and summing over the groups, one rounding to out_type.
  *   a: codes [m, k]; sa: fp32 [m, ceil(k/128)]; w: codes [n, k]; sw: fp32
  *   [ceil(n/128), ceil(k/128)]; bias: bf16 [n] or NULL; out: [m, n].
  * k: a multiple of 16, at least 16 (a and w rows on 16-byte boundaries); m
  * and n any.  sa, sw, bias and out need only their element's alignment.  The
  * same call gives the same bits; where k is split between blocks (and so the
- * order of the fp32 sums over the groups) is chosen by m, n, k and the
- * alignment of a, w and out.  A device-side wait that exceeds its bound leaves its
+ * order of the fp32 sums over the groups) is chosen by m, n, k, the alignment of
+ * a, w and out and the device's number of multiprocessors.  A device-side wait that exceeds its bound leaves its
  * part of `out` unspecified and is reported by fm_ops_sync. */
 fm_status fm_gemm_e4m3_b128(const uint8_t *a, int64_t lda, const float *sa, int64_t ldsa,
                             const uint8_t *w, int64_t ldw, const float *sw, int64_t ldsw,

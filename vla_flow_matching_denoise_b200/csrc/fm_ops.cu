@@ -240,8 +240,12 @@ __global__ void norm_kernel(const NormParams p) {
 template <typename TX, typename TH>
 cudaError_t launch_norm(NormParams p, cudaStream_t st) {
   // One piece of 8 per lane and row needs wpr = d / 256 warps; four pieces per
-  // lane quarter that.  Few rows are spread over warps (latency: 1 x 1024 2.0
-  // us), many keep four pieces, whose groups share their divisions.
+  // lane quarter that.  Few rows are spread over warps (64 x 1024: one piece 2.1,
+  // four 2.8 us; 64 x 4096 2.6, 3.1), many keep four pieces, whose groups share
+  // their divisions (16384 x 1024: 24.7, 21.0 us; 16384 x 2048 47.3, 38.2; 4096 x
+  // 8192 with two 42.8, 38.4).  Around 512 rows the two differ by 10 % either
+  // way.  Rows of less than 1024, whose four pieces are partly empty, lose by it
+  // (16384 x 128: 6.6, 10.8 us; 16384 x 512 with two 12.0, 14.1).
   const int pieces = p.d >> 3;
   int np = pieces > 32 * 16 * 2 ? 4 : pieces > 32 * 16 ? 2 : 1;
   if (p.rows > 512) np = 4;
@@ -458,7 +462,9 @@ cudaError_t launch_gated_u(GatedParams p, fm_act act, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_gated(GatedParams p, fm_act act, int sms, cudaStream_t st) {
   p.row_pieces = ((p.f + 127) / 128) * 16;
-  // Where there are pieces for several waves of threads, each takes UU of them.
+  // Where there are pieces for several waves of threads, each takes UU of them
+  // (SiLU, bf16, f 4096: 592 rows, a quarter of the bound, 4.6 us with one and with
+  // four; at the bound 13.2, 11.1; at four times it 45.4, 34.0).
   constexpr int UU = sizeof(T) == 2 ? 4 : 2;
   return (int64_t)p.rows * p.row_pieces >= (int64_t)sms * 2048 * UU ? launch_gated_u<T, UU>(p, act, st)
                                                                     : launch_gated_u<T, 1>(p, act, st);
@@ -635,8 +641,13 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeP
 template <typename T>
 cudaError_t launch_rope(RopeParams& p, int v, int sms, cudaStream_t st) {
   const int per = p.n / v, heads = p.nq + p.nkv;
-  // one head per thread where rows are few, kHeads or a few times that where
-  // they fill the GPU; whole rows up to about 128 threads per block
+  // One head per thread where rows are few, kHeads or a few times that where
+  // they fill the GPU: as many shares of the heads as bring 1536 threads to an SM
+  // (16 + 2 heads of 128: 306 rows in 18 shares 2.5, in 6 2.7 us; 2048 rows in 6
+  // 7.6, in 2 9.5, in 18 10.6; 16384 rows in 2 31.9, in 1 38.4, in 9 45.0).  The
+  // choice is off by up to 30 % around 1024 rows (18 shares 5.8, 6 4.5).  Whole
+  // rows up to about 128 threads per block (16384 rows: 64 threads 32.1, 128 31.9,
+  // 256 38.3).
   int64_t parts = ((int64_t)sms * 1536 + (int64_t)p.rows * per - 1) / ((int64_t)p.rows * per);
   const int64_t most_parts = (int64_t)p.rows * per * heads < (int64_t)sms * 1024 ? heads : (heads + kHeads - 1) / kHeads;
   if (parts > most_parts) parts = most_parts;
@@ -731,12 +742,6 @@ int sm_count(int device) {
 }  // namespace fm
 
 using fm::OpCheck;
-
-#define FM_TRY(expr)                   \
-  do {                                 \
-    const fm_status st_ = (expr);      \
-    if (st_ != FM_OK) return st_;      \
-  } while (0)
 
 extern "C" {
 #pragma GCC visibility push(default)

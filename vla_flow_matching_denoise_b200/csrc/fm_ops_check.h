@@ -56,3 +56,10 @@ cudaError_t launch_op(void (*kernel)(Params...), unsigned grid, int block, size_
 int sm_count(int device);
 
 }  // namespace fm
+
+// Leaves a call with the first status that is not FM_OK.
+#define FM_TRY(expr)              \
+  do {                            \
+    const fm_status st_ = (expr); \
+    if (st_ != FM_OK) return st_; \
+  } while (0)

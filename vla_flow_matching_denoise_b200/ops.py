@@ -13,7 +13,8 @@ are what Expert.set_prefix takes ([batch, P, n_kv, hd] bf16).
 
 Calls run on the tensors' device, on its current stream (or `stream`), are
 asynchronous and can be captured in a CUDA graph.  Outputs are new tensors
-unless given.  The kernels are in libfm_expert.so, shapes and types are
+unless given; a given one must not overlap an input or another output but where
+its call says so.  The kernels are in libfm_expert.so, shapes and types are
 checked in _ops.so (csrc/fm_ops_torch.cpp), and a missing library raises.  The
 operators have no derivative: a tensor that requires grad is refused while
 gradients are being recorded, one with a forward-mode tangent always.  Writing a
