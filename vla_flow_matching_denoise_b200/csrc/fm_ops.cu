@@ -131,7 +131,7 @@ struct Groups {
 // ----------------------------------------------------------------- residual + RMS norm
 // A row stays in the registers of its `wpr` warps between the sum of squares
 // and the codes: one pass over memory, 8 elements per lane and piece.  Memory
-// bounds it: 38.0 us at 16384 x 2048 bf16 with a residual (6.2 TB/s, 96 % of the
+// bounds it: 38.5 us at 16384 x 2048 bf16 with a residual (6.1 TB/s, 95 % of the
 // measured copy rate), 43.2 before the groups were divided together.
 struct NormParams {
   const void* x;

@@ -468,7 +468,7 @@ cudaError_t launch_few(const CUtensorMap& ma, const CUtensorMap& mw, const GemmP
 // two TMEM accumulators per half; four epilogue warps per half and block
 // scale and sum them, thread = row, so a group's factor is one register.
 // Outputs leave through shared memory, by TMA where `out` allows it (other
-// rows cost ~4000 cycles a tile more: 38.8 -> 66 us at m 12000, k 512, n 4096
+// rows cost ~4000 cycles a tile more: 34.5 -> 60.1 us at m 12000, k 512, n 4096
 // -> 4097).
 //
 // What bounds it: a group is 512 cycles of products and takes 635 (8192^3 in
